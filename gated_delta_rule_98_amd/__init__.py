@@ -1,7 +1,9 @@
 """KDA fp32 recurrent-state decode, speculative verify and replay commit on MI355X.
 
 The computation lives in hand-written HIP kernels for gfx950 behind the C ABI
-of include/kda.h (libkda.so, built in this directory). This package is the thin
+of include/kda.h (libkda.so, built in this directory). Beside it stand linear
+attention with a decay per head on the same slot cache (include/kda_linear.h)
+and the norms around a block (include/kda_norm.h). This package is the thin
 torch-facing binding of that library.
 """
 
@@ -44,4 +46,15 @@ from .kda import (  # noqa: F401
     kda_status_str,
     kda_verify_chunk,
     load_library,
+)
+from .linear import (  # noqa: F401
+    kda_lin_decode_step,
+    kda_lin_prefill,
+    kda_lin_prefill_workspace,
+)
+from .norm import (  # noqa: F401
+    KDA_NORM_MAX_D,
+    KDA_NORM_RESID_BF16,
+    KDA_NORM_Y_BF16,
+    kda_block_norm,
 )

@@ -3,8 +3,9 @@ benchmark's HBM ceiling probes, gated_delta_rule_98_amd/libkda_ceiling.so.
 
 Sources (csrc/): kda_engine.h holds the device building blocks every kernel
 shares; kda_decode.hip, kda_verify.hip, kda_verify_chunk.hip, kda_prefill.hip,
-kda_prefill_chunk.hip and kda_state.hip hold the kernels; kda_api.hip holds
-the C ABI of include/kda.h. Flags:
+kda_prefill_chunk.hip and kda_state.hip hold the KDA kernels, kda_linear.hip
+linear attention and kda_norm.hip the block norm; kda_api.hip holds the C ABI of
+include/kda.h, kda_linear.h and kda_norm.h. Flags:
   -ffp-contract=off   no implicit FMA contraction: every FMA is written out, so
                       all kernels round identically
   -Xclang -target-feature -Xclang -packed-fp32-ops
@@ -22,8 +23,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("kda_api.hip", "kda_decode.hip", "kda_verify.hip",
                                            "kda_verify_chunk.hip", "kda_prefill.hip", "kda_prefill_chunk.hip",
-                                           "kda_state.hip")]
-HEADERS = [os.path.join(CSRC, "kda_engine.h"), os.path.join(ROOT, "include", "kda.h")]
+                                           "kda_state.hip", "kda_linear.hip", "kda_norm.hip")]
+HEADERS = [os.path.join(CSRC, "kda_engine.h"), os.path.join(ROOT, "include", "kda.h"),
+           os.path.join(ROOT, "include", "kda_linear.h"), os.path.join(ROOT, "include", "kda_norm.h")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkda.so")
 # the benchmark's ceiling probes (csrc/probe/): not part of the KDA library or its C ABI

@@ -1,6 +1,6 @@
-// kda_api.hip - the C ABI of include/kda.h: host-side argument checks, the
-// launch shape from (B, H), and dispatch to the kernel tables of the kernel
-// files. Every entry point validates on the host, then enqueues on the
+// kda_api.hip - the C ABI of include/kda.h, kda_linear.h and kda_norm.h:
+// host-side argument checks, the launch shape from (B, H), and dispatch to the
+// kernel tables of the kernel files. Every entry point validates on the host, then enqueues on the
 // caller's stream; nothing here allocates or synchronizes.
 
 #include <string.h>
@@ -9,6 +9,9 @@
 
 #include "kda_chunk.h"
 #include "kda_engine.h"
+#include "kda_linear.h"
+#include "kda_linear_impl.h"
+#include "kda_norm.h"
 
 using namespace kda;
 
@@ -663,6 +666,200 @@ int kda_state_unpack(float *cache, int64_t num_slots, int64_t slot_stride, const
                      int32_t ncols, const float *buf, int32_t *dev_err, void *stream) {
   return state_copy(false, cache, num_slots, slot_stride, slot_ids, B, H, dk, dv, head0, nheads, col0, ncols,
                     const_cast<float *>(buf), dev_err, stream);
+}
+
+// ------------------------------------------------------------------ linear attention
+
+// The token inputs of a linear-attention call.
+static int check_lin_tokens(const kda_lin_tokens *x, int32_t H, int32_t dk, int32_t dv) {
+  if (!x || !x->q || !x->k || !x->v || !x->alpha || x->Hk <= 0 || H % x->Hk != 0) return KDA_ERR_INVALID;
+  const int64_t kw = (int64_t)x->Hk * dk, vw = (int64_t)H * dv;
+  if (x->q_stride < kw || x->k_stride < kw || x->v_stride < vw) return KDA_ERR_INVALID;
+  if (x->alpha_stride != 0 && x->alpha_stride < H) return KDA_ERR_INVALID;
+  if (!aligned(x->q, 16) || !aligned(x->k, 16) || !aligned(x->v, 16) || !aligned(x->alpha, 4) ||
+      x->q_stride % 8 != 0 || x->k_stride % 8 != 0 || x->v_stride % 8 != 0)
+    return KDA_ERR_ALIGN;
+  return KDA_OK;
+}
+
+// Flags and verify_form of a linear-attention call; *bf16: the output's type.
+static int lin_options(const kda_options *opts, int32_t *bf16) {
+  Args f;
+  memset(&f, 0, sizeof f);
+  KDA_TRY(read_flags(opts, KDA_RAW_INPUTS | KDA_OUT_BF16, f));
+  if (opts && opts->verify_form != 0) return KDA_ERR_INVALID;
+  if (f.raw) return KDA_ERR_UNSUPPORTED;
+  *bf16 = f.out_bf16;
+  return KDA_OK;
+}
+
+static int check_lin_out(const void *out, int32_t bf16) {
+  if (!out) return KDA_ERR_INVALID;
+  return aligned(out, bf16 ? 8 : 16) ? KDA_OK : KDA_ERR_ALIGN;
+}
+
+static void set_lin_tokens(LinArgs &a, const kda_lin_tokens *x, int32_t H) {
+  a.q = x->q;
+  a.k = x->k;
+  a.v = x->v;
+  a.alpha = x->alpha;
+  a.qs = x->q_stride;
+  a.ks = x->k_stride;
+  a.vs = x->v_stride;
+  a.as = x->alpha_stride;
+  a.group = H / x->Hk;
+}
+
+static int launch_lin(const void *fn, int64_t blocks, int threads, LinArgs &a, void *stream) {
+  if (!fn || blocks > 0x7fffffff) return KDA_ERR_UNSUPPORTED;
+  void *args[] = {&a};
+  const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(threads), args, 0, (hipStream_t)stream);
+  return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+int kda_lin_decode_step(float *cache, int64_t num_slots, int64_t slot_stride, const int32_t *slot_ids, int32_t B,
+                        int32_t H, int32_t dk, int32_t dv, const kda_lin_tokens *x, void *out,
+                        const kda_epilogue *epi, int32_t *dev_err, const kda_options *opts, void *stream) {
+  LinArgs a;
+  memset(&a, 0, sizeof a);
+  if (B < 0 || H <= 0 || dk <= 0 || dv <= 0) return KDA_ERR_INVALID;
+  KDA_TRY(lin_options(opts, &a.out_bf16));
+  if (!dims_supported(dk, dv)) return KDA_ERR_UNSUPPORTED;
+  if (B == 0) return KDA_OK;
+  if (!slot_ids) return KDA_ERR_INVALID;
+  KDA_TRY(check_slots(opts, slot_ids, B));
+  KDA_TRY(check_cache(cache, num_slots, slot_stride, H, dk, dv));
+  KDA_TRY(check_lin_tokens(x, H, dk, dv));
+  KDA_TRY(check_lin_out(out, a.out_bf16));
+  KDA_TRY(check_gate(epi));
+  if (!aligned(slot_ids, 4) || (dev_err && !aligned(dev_err, 4))) return KDA_ERR_ALIGN;
+  Launch l;
+  const int tile_w = opts ? opts->tile_w : 0;
+  if (tile_w == 2) return KDA_ERR_UNSUPPORTED;
+  KDA_TRY(choose_width(KIND_DECODE, B, H, dk, dv, epi != nullptr, tile_w, &l));
+  if (l.C == 0) KDA_TRY(choose_width(KIND_DECODE, B, H, dk, dv, false, 4, &l));
+
+  a.cache = cache;
+  a.num_slots = num_slots;
+  a.slot_stride = slot_stride;
+  a.slot_ids = slot_ids;
+  set_lin_tokens(a, x, H);
+  a.out = out;
+  a.gate = epi ? epi->gate : nullptr;
+  a.weight = epi ? epi->weight : nullptr;
+  a.eps = epi ? epi->eps : 0.0f;
+  a.dev_err = dev_err;
+  a.B = B;
+  a.H = H;
+  a.dv = dv;
+  a.ntile = dv / l.W;
+  return launch_lin(lin_decode_kernel_for(dk, l.C, epi != nullptr, a.out_bf16), (int64_t)B * H * a.ntile, 64 * l.waves,
+                    a, stream);
+}
+
+int kda_lin_prefill_workspace(int32_t B, int32_t n_tok, int32_t H, int32_t dk, int32_t dv, size_t *bytes) {
+  if (!bytes || B < 0 || n_tok < 0 || H <= 0 || dk <= 0 || dv <= 0) return KDA_ERR_INVALID;
+  if (!dims_supported(dk, dv)) return KDA_ERR_UNSUPPORTED;
+  *bytes = 0;
+  return KDA_OK;
+}
+
+int kda_lin_prefill(float *cache, int64_t num_slots, int64_t slot_stride, const int32_t *slot_ids,
+                    const int32_t *cu_seqlens, int32_t B, int32_t n_tok, int32_t H, int32_t dk, int32_t dv,
+                    const kda_lin_tokens *x, void *out, const int32_t *ckpt_pos, float *ckpt, void *workspace,
+                    size_t workspace_bytes, int32_t *dev_err, const kda_options *opts, void *stream) {
+  LinArgs a;
+  memset(&a, 0, sizeof a);
+  if (B < 0 || H <= 0 || dk <= 0 || dv <= 0 || n_tok < 0) return KDA_ERR_INVALID;
+  KDA_TRY(lin_options(opts, &a.out_bf16));
+  if (!dims_supported(dk, dv) || (opts && opts->tile_w != 0)) return KDA_ERR_UNSUPPORTED;
+  if (B == 0 || (n_tok == 0 && !ckpt_pos)) return KDA_OK;
+  if (!slot_ids || !cu_seqlens) return KDA_ERR_INVALID;
+  KDA_TRY(check_slots(opts, slot_ids, B));
+  KDA_TRY(check_cache(cache, num_slots, slot_stride, H, dk, dv));
+  if (n_tok > 0) {
+    KDA_TRY(check_lin_tokens(x, H, dk, dv));
+    KDA_TRY(check_lin_out(out, a.out_bf16));
+    set_lin_tokens(a, x, H);
+  }
+  if (ckpt_pos) {
+    if (!ckpt) return KDA_ERR_INVALID;
+    if (!aligned(ckpt, 16) || !aligned(ckpt_pos, 4)) return KDA_ERR_ALIGN;
+  }
+  if (!aligned(slot_ids, 4) || !aligned(cu_seqlens, 4) || (dev_err && !aligned(dev_err, 4))) return KDA_ERR_ALIGN;
+  size_t need = 0;
+  KDA_TRY(kda_lin_prefill_workspace(B, n_tok, H, dk, dv, &need));
+  if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_INVALID;
+  if (need > 0 && !aligned(workspace, 16)) return KDA_ERR_ALIGN;
+
+  a.cache = cache;
+  a.num_slots = num_slots;
+  a.slot_stride = slot_stride;
+  a.slot_ids = slot_ids;
+  a.cu = cu_seqlens;
+  a.ckpt_pos = ckpt_pos;
+  a.out = out;
+  a.ckpt = ckpt;
+  a.dev_err = dev_err;
+  a.B = B;
+  a.H = H;
+  a.dv = dv;
+  a.n_tok = n_tok;
+  a.ntile = dv / 16;
+  return launch_lin(lin_prefill_kernel_for(dk), (int64_t)B * H * a.ntile, 256, a, stream);
+}
+
+// ------------------------------------------------------------------ block norm
+
+int kda_block_norm(const void *resid, int64_t resid_stride, const uint16_t *z, int64_t z_stride, void *resid_out,
+                   int64_t resid_out_stride, void *y, int64_t y_stride, const float *w_post, const uint16_t *gate,
+                   int64_t gate_stride, float res_scale, const float *w_pre, float eps, int32_t rows, int32_t D,
+                   int32_t flags, void *stream) {
+  if (rows < 0 || D <= 0 || (flags & ~(int32_t)(KDA_NORM_RESID_BF16 | KDA_NORM_Y_BF16))) return KDA_ERR_INVALID;
+  if (!(eps >= 0.0f) || eps > 3.0e38f || !(res_scale >= -3.0e38f && res_scale <= 3.0e38f)) return KDA_ERR_INVALID;
+  if (D > KDA_NORM_MAX_D) return KDA_ERR_UNSUPPORTED;
+  if (rows == 0) return KDA_OK;
+  if (!resid || (!z && !y) || (y == nullptr) != (w_pre == nullptr)) return KDA_ERR_INVALID;
+  if (z ? !resid_out : (resid_out || w_post || gate)) return KDA_ERR_INVALID;
+  if (resid_stride < D || (z && (z_stride < D || resid_out_stride < D)) || (y && y_stride < D) ||
+      (gate && gate_stride < D))
+    return KDA_ERR_INVALID;
+  if (resid_out == resid && resid_out_stride != resid_stride) return KDA_ERR_INVALID;
+  const int rb = flags & KDA_NORM_RESID_BF16 ? 2 : 4, yb = flags & KDA_NORM_Y_BF16 ? 2 : 4;
+  if (!aligned(resid, rb) || !aligned(resid_out, rb) || !aligned(y, yb) || !aligned(z, 2) || !aligned(gate, 2) ||
+      !aligned(w_post, 4) || !aligned(w_pre, 4))
+    return KDA_ERR_ALIGN;
+  const auto row16 = [](const void *p, int64_t stride, int bytes) {
+    return !p || (aligned(p, 16) && stride * bytes % 16 == 0);
+  };
+  const bool vec = D % 8 == 0 && row16(resid, resid_stride, rb) && row16(resid_out, resid_out_stride, rb) &&
+                   row16(z, z_stride, 2) && row16(gate, gate_stride, 2) && row16(y, y_stride, yb) &&
+                   row16(w_post, 0, 4) && row16(w_pre, 0, 4);
+  NormArgs a;
+  memset(&a, 0, sizeof a);
+  a.resid = resid;
+  a.z = z;
+  a.gate = gate;
+  a.resid_out = resid_out;
+  a.y = y;
+  a.w_post = w_post;
+  a.w_pre = w_pre;
+  a.rs = resid_stride;
+  a.zs = z_stride;
+  a.ros = resid_out_stride;
+  a.ys = y_stride;
+  a.gs = gate_stride;
+  a.scale = res_scale;
+  a.eps = eps;
+  a.rows = rows;
+  a.D = D;
+  a.resid_bf16 = rb == 2;
+  a.y_bf16 = yb == 2;
+  int threads = 0;
+  const void *fn = norm_kernel_for(D, vec, &threads);
+  void *args[] = {&a};
+  const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)rows), dim3(threads), args, 0, (hipStream_t)stream);
+  return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 
 const char *kda_status_str(int32_t status) {

@@ -1,0 +1,45 @@
+// kda_linear_impl.h - interface of the linear-attention kernels (kda_linear.hip)
+// and the block norm (kda_norm.hip) to the C ABI in kda_api.hip.
+
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+namespace kda {
+
+// Arguments of the linear-attention kernels.
+struct LinArgs {
+  float *cache;
+  int64_t num_slots, slot_stride;
+  const int32_t *slot_ids, *cu, *ckpt_pos;
+  const uint16_t *q, *k, *v, *gate;
+  const float *alpha, *weight;
+  int64_t qs, ks, vs, as;  // elements between tokens
+  void *out;               // fp32, or bf16 when out_bf16
+  float *ckpt;
+  int32_t *dev_err;
+  float eps;
+  int32_t B, H, group, dv, n_tok, ntile;  // group = H / Hk heads share a key head
+  int32_t out_bf16;
+};
+
+const void *lin_decode_kernel_for(int dk, int C, bool gate, bool bf16);
+const void *lin_prefill_kernel_for(int dk);
+
+// Arguments of the block norm.
+struct NormArgs {
+  const void *resid;
+  const uint16_t *z, *gate;
+  void *resid_out, *y;
+  const float *w_post, *w_pre;
+  int64_t rs, zs, ros, ys, gs;
+  float scale, eps;
+  int32_t rows, D, resid_bf16, y_bf16;
+};
+
+// Launch shape and kernel of a block norm of width D (vec: every row is 16-byte
+// aligned and D is a multiple of 8).
+const void *norm_kernel_for(int D, bool vec, int *threads);
+
+}  // namespace kda

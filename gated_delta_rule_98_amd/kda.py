@@ -107,6 +107,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.kda_query_variant.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32,
                                       ctypes.POINTER(i32), ctypes.POINTER(i32)]
     lib.kda_query_variant.restype = ctypes.c_int
+    lib.kda_lin_decode_step.argtypes = [P, i64, i64, P, i32, i32, i32, i32, P, P, P, P, P, P]
+    lib.kda_lin_decode_step.restype = ctypes.c_int
+    lib.kda_lin_prefill.argtypes = [P, i64, i64, P, P, i32, i32, i32, i32, i32, P, P, P, P, P, ctypes.c_size_t,
+                                    P, P, P]
+    lib.kda_lin_prefill.restype = ctypes.c_int
+    lib.kda_lin_prefill_workspace.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)]
+    lib.kda_lin_prefill_workspace.restype = ctypes.c_int
+    lib.kda_block_norm.argtypes = [P, i64, P, i64, P, i64, P, i64, P, P, i64, ctypes.c_float, P, ctypes.c_float,
+                                   i32, i32, i32, P]
+    lib.kda_block_norm.restype = ctypes.c_int
     lib.kda_status_str.argtypes = [i32]
     lib.kda_status_str.restype = ctypes.c_char_p
     _lib = lib
