@@ -5,6 +5,7 @@
 
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "kda_chunk.h"
@@ -757,10 +758,33 @@ int kda_lin_decode_step(float *cache, int64_t num_slots, int64_t slot_stride, co
                     a, stream);
 }
 
+// Chunks per segment of a prefill and the segments past the rows' first ones.
+// A segment is long enough that about 512 (unit, head) workgroups share the
+// chunks, two per CU, and at least 4 chunks. Rows that hold at most that many
+// are one segment. A row of n tokens has at most (n - 1) / 64 chunks after its
+// first, so the rows together have at most n_tok / 64 / seg segments after
+// their first ones.
+struct LinSplit {
+  int32_t seg;
+  int64_t more;
+};
+
+static LinSplit lin_split(int32_t B, int32_t n_tok, int32_t H) {
+  const int64_t chunks = (int64_t)n_tok / kLinChunk + B;
+  const int64_t seg = std::min<int64_t>(std::max<int64_t>(4, (chunks * H + 511) / 512), 1 << 24);
+  return {(int32_t)seg, n_tok / kLinChunk / seg};
+}
+
+static size_t lin_ws_state_bytes(const LinSplit &s, int32_t H, int32_t dk, int32_t dv) {
+  return (size_t)(2 * s.more) * H * dk * dv * sizeof(float);
+}
+
 int kda_lin_prefill_workspace(int32_t B, int32_t n_tok, int32_t H, int32_t dk, int32_t dv, size_t *bytes) {
   if (!bytes || B < 0 || n_tok < 0 || H <= 0 || dk <= 0 || dv <= 0) return KDA_ERR_INVALID;
   if (!dims_supported(dk, dv)) return KDA_ERR_UNSUPPORTED;
-  *bytes = 0;
+  const LinSplit s = lin_split(B, n_tok, H);
+  // a state for every segment of a row that has two or more, then their decays
+  *bytes = lin_ws_state_bytes(s, H, dk, dv) + ((size_t)(2 * s.more) * H * sizeof(float) + 15) / 16 * 16;
   return KDA_OK;
 }
 
@@ -805,8 +829,21 @@ int kda_lin_prefill(float *cache, int64_t num_slots, int64_t slot_stride, const 
   a.H = H;
   a.dv = dv;
   a.n_tok = n_tok;
-  a.ntile = dv / 16;
-  return launch_lin(lin_prefill_kernel_for(dk), (int64_t)B * H * a.ntile, 256, a, stream);
+  const LinSplit s = lin_split(B, n_tok, H);
+  a.seg = s.seg;
+  const int64_t units = B + s.more;
+  if (units * H > 0x7ffffff0) return KDA_ERR_UNSUPPORTED;
+  a.units = (int32_t)units;
+  a.ws = static_cast<float *>(workspace);
+  a.wdec = reinterpret_cast<float *>(static_cast<char *>(workspace) + lin_ws_state_bytes(s, H, dk, dv));
+  if (n_tok == 0) a.group = 1;  // no tokens, no key heads
+  // units x key heads dealt to the 8 XCDs, the heads of a key head together
+  const int64_t blocks = (units * (H / a.group) + 7) / 8 * 8 * a.group;
+  if (s.more > 0) {
+    KDA_TRY(launch_lin(lin_sum_kernel_for(dk, dv), blocks, kLinThreads, a, stream));
+    KDA_TRY(launch_lin(lin_scan_kernel_for(dk, dv), (int64_t)B * H * lin_scan_parts(dk, dv), kLinThreads, a, stream));
+  }
+  return launch_lin(lin_out_kernel_for(dk, dv, a.out_bf16), blocks, kLinThreads, a, stream);
 }
 
 // ------------------------------------------------------------------ block norm

@@ -93,49 +93,665 @@ __global__ __launch_bounds__(GATE ? 1024 : 256) void lin_decode_kernel(LinArgs a
   }
 }
 
-// Prompts, token by token: one workgroup per (row, head, 16 value columns).
-template <int DK>
-__global__ __launch_bounds__(256) void lin_prefill_kernel(LinArgs a) {
-  constexpr int NV = DK / 64;
-  const Unit u = unit_of_block_rows(a.ntile, a.H, a.B);
-  const Lane L = lane_geometry();
-  const int32_t slot = a.slot_ids[u.b], c0 = a.cu[u.b], c1 = a.cu[u.b + 1];
-  if (slot < 0) return;
-  if (slot >= a.num_slots) {
-    report(a.dev_err, u, KDA_DEVERR_SLOT);
-    return;
-  }
-  if (c0 < 0 || c1 < c0 || c1 > a.n_tok) {
-    report(a.dev_err, u, KDA_DEVERR_SEQLEN);
-    return;
-  }
-  const int ck = a.ckpt_pos ? a.ckpt_pos[u.b] : -1;
-  if (ck > c1 - c0) {
-    report(a.dev_err, u, KDA_DEVERR_CKPT);
-    return;
-  }
-  const int64_t col = (int64_t)u.h * a.dv + u.tile * 16;
-  float *S = a.cache + (int64_t)slot * a.slot_stride + col * DK;
-  float *CK = ck >= 0 ? a.ckpt + ((int64_t)u.b * a.H * a.dv + col) * DK : nullptr;
-  float4 s[1][NV];
-  load_tile<DK, 1, false>(s, S, L);
-  if (ck == 0) store_tile<DK, 1, false>(CK, s, L);
-  for (int t = c0; t < c1; ++t) {
-    float4 kk[NV], qq[NV];
+// ----------------------------------------------------------------------------
+// Prompts in chunk form
+// ----------------------------------------------------------------------------
+//
+// A row is cut into chunks of 64 tokens. With S0 the state entering a chunk,
+// Gamma_t the product of its decays up to and including token t and D(t, s) the
+// product of those after s up to t, the recurrence unrolls to
+//     o_t = Gamma_t S0^T q_t + sum_{s <= t} D(t, s) (k_s . q_t) v_s
+//     S_L = Gamma_L S0 + sum_s D(L, s) k_s v_s^T
+// The decay is a scalar, so it scales scores and tokens and no triangular
+// system has to be solved: the sum in S_L does not depend on S0. Long rows are
+// therefore cut into segments of whole chunks that run in parallel: one kernel
+// takes every segment's state sum (from a zero state), a second chains them to
+// the state that enters each segment, and a third runs each segment from that
+// state and writes the outputs. Rows of one segment need the third kernel only.
+//
+// Products on the bfloat16 matrix cores at fp32 accuracy. q, k and v are exact
+// in bfloat16. The other operand of a product (the state, the decayed scores,
+// the tokens scaled to the chunk's end) is fp32 and is split by truncation into
+// three bfloat16 parts, 8 + 8 + 8 bits of its 24, which is exact; the three
+// products are exact in fp32 and accumulate there.
+//
+// Decay products never divide and never go through logarithms: a block of 16
+// tokens holds prefix products, suffix products and its own product, and D(t, s)
+// across blocks is prefix * (blocks between) * suffix. A product underflows
+// only where the true value does, and 0 or a negative decay is like any other.
+// Gamma and the decay to the chunk's end carry across chunks, so they are
+// formed in 64 bits and rounded once.
+
+constexpr int kLB = 16;                // block: the MFMA tile
+constexpr int kLP = kLinChunk + 8;     // row pitch of the scores, padded against bank conflicts
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+struct Split3 {
+  bf16x8 hi, mid, lo;
+};
+
+// One word of two bfloat16: the upper halves of x0 (low) and x1 (high).
+__device__ __forceinline__ uint32_t upper_pair(float x0, float x1) {
+  return __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302u);
+}
+
+__device__ __forceinline__ float below_upper(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+
+// words[0..N/2) the high, [N/2..N) the middle and [N..3N/2) the low parts of x
+template <int N>
+__device__ __forceinline__ void split3_words(const float (&x)[N], uint32_t (&w)[3 * N / 2]) {
 #pragma unroll
-    for (int e = 0; e < NV; ++e) {
-      const int64_t i = (int64_t)(u.h / a.group) * DK + 4 * L.r + 64 * e;
-      kk[e] = unpack_bf16x4(*reinterpret_cast<const uint2 *>(a.k + t * a.ks + i));
-      qq[e] = unpack_bf16x4(*reinterpret_cast<const uint2 *>(a.q + t * a.qs + i));
-    }
-    const float vj[1] = {bf16_to_f32(a.v[t * a.vs + col + L.col0])};
-    const float al = a.alpha[t * a.as + u.h];
-    float o[1];
-    lin_token<NV, 1>(s, kk, qq, vj, al, o);
-    if (L.r == 0) lin_put(a, a.out_bf16, (int64_t)t * a.H * a.dv + col + L.col0, o[0]);
-    if (t + 1 - c0 == ck) store_tile<DK, 1, false>(CK, s, L);
+  for (int i = 0; i < N / 2; ++i) {
+    float x0 = x[2 * i], x1 = x[2 * i + 1];
+    w[i] = upper_pair(x0, x1);
+    x0 = below_upper(x0);
+    x1 = below_upper(x1);
+    w[N / 2 + i] = upper_pair(x0, x1);
+    w[N + i] = upper_pair(below_upper(x0), below_upper(x1));
   }
-  store_tile<DK, 1, false>(S, s, L);
+}
+
+__device__ __forceinline__ Split3 split3(const float (&x)[8]) {
+  uint32_t w[12];
+  split3_words<8>(x, w);
+  return {__builtin_bit_cast(bf16x8, (u32x4){w[0], w[1], w[2], w[3]}),
+          __builtin_bit_cast(bf16x8, (u32x4){w[4], w[5], w[6], w[7]}),
+          __builtin_bit_cast(bf16x8, (u32x4){w[8], w[9], w[10], w[11]})};
+}
+
+__device__ __forceinline__ v4f mma(bf16x8 a, bf16x8 b, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// c + (hi + mid + lo) b and c + a (hi + mid + lo), small terms first
+__device__ __forceinline__ v4f mma3(const Split3 &a, bf16x8 b, v4f c) {
+  return mma(a.hi, b, mma(a.mid, b, mma(a.lo, b, c)));
+}
+__device__ __forceinline__ v4f mma3(bf16x8 a, const Split3 &b, v4f c) {
+  return mma(a, b.hi, mma(a, b.mid, mma(a, b.lo, c)));
+}
+
+// An MFMA operand whose contraction index runs over tokens, from a token-major
+// LDS array: lane (m, g) gets column m of its 16 at tokens 8 g .. 8 g + 7. Each
+// 16-lane group reads 4 tokens x 16 columns (lane i the 4 columns 4 (i % 4) of
+// token i / 4) and the transposing read hands lane i column i of the 4 tokens.
+template <int PITCH>
+__device__ __forceinline__ bf16x8 ld_tokens(const uint16_t *base, int tok0, int col0) {
+  typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
+  const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
+  const uint16_t *p = base + (tok0 + 8 * g + (i >> 2)) * PITCH + col0 + 4 * (i & 3);
+  const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)p);
+  const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * PITCH));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// 8 channels of one token: contiguous, or the two runs of 4 at which the lane's
+// accumulator registers of two 16-channel tiles stand.
+__device__ __forceinline__ bf16x8 ld_run8(const uint16_t *p) {
+  return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(p));
+}
+__device__ __forceinline__ bf16x8 ld_run4x2(const uint16_t *p) {
+  const u32x2 a = *reinterpret_cast<const u32x2 *>(p), b = *reinterpret_cast<const u32x2 *>(p + 16);
+  return __builtin_bit_cast(bf16x8, (u32x4){a.x, a.y, b.x, b.y});
+}
+
+// x moved over DPP control CTRL inside 16-lane rows, 1 where no lane is the source
+template <int CTRL>
+__device__ __forceinline__ float dpp_or_one(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0x3f800000, __float_as_int(x), CTRL, 0xF, 0xF, false));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_or_one(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0x3ff00000, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Inclusive prefix and suffix products over a 16-lane row.
+template <class T>
+__device__ __forceinline__ T row_prefix(T x) {
+  x = x * dpp_or_one<0x111>(x);
+  x = x * dpp_or_one<0x112>(x);
+  x = x * dpp_or_one<0x114>(x);
+  return x * dpp_or_one<0x118>(x);
+}
+template <class T>
+__device__ __forceinline__ T row_suffix(T x) {
+  x = x * dpp_or_one<0x101>(x);
+  x = x * dpp_or_one<0x102>(x);
+  x = x * dpp_or_one<0x104>(x);
+  return x * dpp_or_one<0x108>(x);
+}
+
+__device__ __forceinline__ double readlane_f64(double x, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// The decays of one chunk, by token.
+struct ChunkDecay {
+  float al[kLinChunk];   // the decay itself (1 past the chunk's end)
+  float suf[kLinChunk];  // product over the token's block after it
+  float gam[kLinChunk];  // Gamma: product over the chunk up to and including it
+  float end[kLinChunk];  // product over the chunk after it
+};
+
+// One wave, lane = token.
+struct LaneDecay {
+  float suf, gam, end;
+};
+__device__ __forceinline__ LaneDecay chunk_decay(float al) {
+  const int row = (threadIdx.x & 63) >> 4;
+  const double p = row_prefix((double)al), s = row_suffix((double)al);
+  const double after = dpp_or_one<0x101>(s);  // the suffix of the next lane
+  const double m0 = readlane_f64(p, 15), m1 = readlane_f64(p, 31), m2 = readlane_f64(p, 47), m3 = readlane_f64(p, 63);
+  const double pre = row == 0 ? 1.0 : row == 1 ? m0 : row == 2 ? m0 * m1 : m0 * m1 * m2;
+  const double post = row == 0 ? m1 * m2 * m3 : row == 1 ? m2 * m3 : row == 2 ? m3 : 1.0;
+  return {(float)after, (float)(p * pre), (float)(after * post)};
+}
+
+__device__ __forceinline__ void put_chunk_decay(ChunkDecay &d, float al) {
+  const int lane = threadIdx.x & 63;
+  const LaneDecay x = chunk_decay(al);
+  d.al[lane] = al;
+  d.suf[lane] = x.suf;
+  d.gam[lane] = x.gam;
+  d.end[lane] = x.end;
+}
+
+// One row's tokens and its place in the numbering of units: a row has
+// max(1, ceil(chunks / seg)) units (one segment each; a row to skip has one,
+// which reports it), and a state slot per segment if it has more than one.
+// Units 0 .. a.units - 1 are launched, which holds every row of a table whose
+// rows do not overlap; a row past them is skipped and reported as a bad range.
+struct LinRow {
+  int b, unit0, slot0, nseg, n;
+  int32_t c0, slot;
+  int err;  // 0, a device error, or -1 for a padding row
+};
+
+__device__ __forceinline__ int lin_row_check(const LinArgs &a, int b, int32_t &slot, int32_t &c0, int &n) {
+  slot = a.slot_ids[b];
+  c0 = a.cu[b];
+  const int32_t c1 = a.cu[b + 1];
+  n = 0;
+  if (slot < 0) return -1;
+  if (slot >= a.num_slots) return KDA_DEVERR_SLOT;
+  if (c0 < 0 || c1 < c0 || c1 > a.n_tok) return KDA_DEVERR_SEQLEN;
+  if (a.ckpt_pos && a.ckpt_pos[b] > c1 - c0) return KDA_DEVERR_CKPT;
+  n = c1 - c0;
+  return 0;
+}
+
+__device__ __forceinline__ int lin_segments(const LinArgs &a, int n) {
+  const int chunks = (n + kLinChunk - 1) / kLinChunk;
+  return chunks > a.seg ? (chunks + a.seg - 1) / a.seg : 1;
+}
+
+// The row that holds a unit (by_unit) or the row of that number, found by each
+// wave over 64 rows at a time; false where there is none.
+__device__ __forceinline__ bool lin_find(const LinArgs &a, bool by_unit, int key, LinRow &r) {
+  const int lane = threadIdx.x & 63;
+  int units = 0, slots = 0;
+  for (int base = 0; base < a.B; base += 64) {
+    const int b = base + lane;
+    int32_t slot = -1, c0 = 0;
+    int n = 0, err = -1, nseg = 0;
+    if (b < a.B) {
+      err = lin_row_check(a, b, slot, c0, n);
+      nseg = lin_segments(a, n);
+    }
+    int iu = nseg, is = nseg > 1 ? nseg : 0;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int u = __shfl_up(iu, d), s = __shfl_up(is, d);
+      if (lane >= d) {
+        iu += u;
+        is += s;
+      }
+    }
+    const uint64_t hit = __ballot(b < a.B && (by_unit ? key < units + iu : b == key));
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      r.b = base + l;
+      r.nseg = __builtin_amdgcn_readlane(nseg, l);
+      r.unit0 = units + __builtin_amdgcn_readlane(iu, l) - r.nseg;
+      r.slot0 = slots + __builtin_amdgcn_readlane(is, l) - (r.nseg > 1 ? r.nseg : 0);
+      r.n = __builtin_amdgcn_readlane(n, l);
+      r.c0 = __builtin_amdgcn_readlane(c0, l);
+      r.slot = __builtin_amdgcn_readlane(slot, l);
+      r.err = __builtin_amdgcn_readlane(err, l);
+      if (r.err == 0 && r.unit0 + r.nseg > a.units) r.err = KDA_DEVERR_SEQLEN;
+      return true;
+    }
+    units += __builtin_amdgcn_readlane(iu, 63);
+    slots += __builtin_amdgcn_readlane(is, 63);
+  }
+  return false;
+}
+
+// Workgroups are dispatched round-robin over the 8 XCDs. The heads that share a
+// key head, in one unit, are one XCD's, next to each other in its order, so
+// that they read its q and k through one L2.
+__device__ __forceinline__ bool lin_unit_head(const LinArgs &a, int &unit, int &h) {
+  const int n = blockIdx.x, hk = a.H / a.group;
+  int j, in_group;
+  divmod_uniform(n >> 3, a.group, j, in_group);
+  const int g = 8 * j + (n & 7);
+  int kh;
+  divmod_uniform(g, hk, unit, kh);
+  h = kh * a.group + in_group;
+  return unit < a.units;
+}
+
+// Accumulator layout of a state. Wave w of the four holds value columns
+// [w DV/4, (w + 1) DV/4); its register tile [ni][nj] holds key channels
+// 16 ni + 4 g .. + 3 of column 16 nj + m in lane (m, g).
+template <int DK, int DV>
+struct LinState {
+  static constexpr int NI = DK / 16, NJ = DV / 64;
+  v4f s[NI][NJ];
+
+  __device__ static int64_t at(int ni, int nj) {  // element of a [dv][dk] state
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    return (int64_t)(w * (DV / 4) + 16 * nj + (lane & 15)) * DK + 16 * ni + 4 * (lane >> 4);
+  }
+  __device__ static int ws_at(int ni, int nj) {  // element of a state in the workspace, in register order
+    return ((ni * NJ + nj) * kLinThreads + (int)threadIdx.x) * 4;
+  }
+  __device__ __forceinline__ void load(const float *p, bool ws) {
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+      for (int nj = 0; nj < NJ; ++nj)
+        s[ni][nj] = *reinterpret_cast<const v4f *>(p + (ws ? (int64_t)ws_at(ni, nj) : at(ni, nj)));
+  }
+  __device__ __forceinline__ void store(float *p, bool ws) const {
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+      for (int nj = 0; nj < NJ; ++nj)
+        *reinterpret_cast<v4f *>(p + (ws ? (int64_t)ws_at(ni, nj) : at(ni, nj))) = s[ni][nj];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+      for (int nj = 0; nj < NJ; ++nj) s[ni][nj] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+  }
+};
+
+// A chunk of one token array on its way to LDS: 16-byte pieces, zero past the
+// chunk's n tokens.
+template <int D>
+struct Staged16 {
+  static constexpr int N = kLinChunk * D / 8 / kLinThreads, PITCH = D + 8;
+  uint4 x[N];
+
+  __device__ __forceinline__ void load(const uint16_t *base, int64_t stride, int n) {
+#pragma unroll
+    for (int m = 0; m < N; ++m) {
+      const int p = (int)threadIdx.x + kLinThreads * m, t = p / (D / 8), c = (p % (D / 8)) * 8;
+      x[m] = make_uint4(0u, 0u, 0u, 0u);
+      if (t < n) x[m] = *reinterpret_cast<const uint4 *>(base + t * stride + c);
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t *lds) const {
+#pragma unroll
+    for (int m = 0; m < N; ++m) {
+      const int p = (int)threadIdx.x + kLinThreads * m, t = p / (D / 8), c = (p % (D / 8)) * 8;
+      *reinterpret_cast<uint4 *>(lds + t * PITCH + c) = x[m];
+    }
+  }
+};
+
+// The wave's tokens of v: [kb][nj] holds tokens 32 kb + 8 g .. + 7 of column m.
+template <int DV>
+__device__ __forceinline__ void load_values(const uint16_t *vl, bf16x8 (&vr)[2][DV / 64]) {
+  const int w = threadIdx.x >> 6;
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+    for (int nj = 0; nj < DV / 64; ++nj) vr[kb][nj] = ld_tokens<DV + 8>(vl, 32 * kb, w * (DV / 4) + 16 * nj);
+}
+
+// Tokens 32 kb + 8 g .. + 7 of a column, each times its factor f, split.
+__device__ __forceinline__ Split3 scaled_values(bf16x8 v, const float (&f)[8]) {
+  const u32x4 u = __builtin_bit_cast(u32x4, v);
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[2 * e] = __uint_as_float(u[e] << 16) * f[2 * e];
+    x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u) * f[2 * e + 1];
+  }
+  return split3(x);
+}
+
+// S <- Gamma_L S + sum_s end_s k_s v_s^T
+template <int DK, int DV>
+__device__ __forceinline__ void chunk_state(LinState<DK, DV> &S, const uint16_t *kl, const bf16x8 (&vr)[2][DV / 64],
+                                            const ChunkDecay &d) {
+  constexpr int NI = DK / 16, NJ = DV / 64;
+  const int g = (threadIdx.x & 63) >> 4;
+  const float gl = d.gam[kLinChunk - 1];
+#pragma unroll
+  for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+    for (int nj = 0; nj < NJ; ++nj) S.s[ni][nj] *= gl;
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb) {
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = d.end[32 * kb + 8 * g + e];
+    Split3 vs[NJ];
+#pragma unroll
+    for (int nj = 0; nj < NJ; ++nj) vs[nj] = scaled_values(vr[kb][nj], f);
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) {
+      const bf16x8 kt = ld_tokens<DK + 8>(kl, 32 * kb, 16 * ni);
+#pragma unroll
+      for (int nj = 0; nj < NJ; ++nj) S.s[ni][nj] = mma3(kt, vs[nj], S.s[ni][nj]);
+    }
+  }
+}
+
+// The state after the first n tokens of a chunk (0 < n < 64), to ck ([dv][dk]).
+template <int DK, int DV>
+__device__ __forceinline__ void chunk_checkpoint(const LinState<DK, DV> &S, const uint16_t *kl,
+                                                 const bf16x8 (&vr)[2][DV / 64], const ChunkDecay &d, int n, float *ck) {
+  constexpr int NI = DK / 16, NJ = DV / 64;
+  const int lane = threadIdx.x & 63, g = lane >> 4;
+  const LaneDecay x = chunk_decay(lane < n ? d.al[lane] : 1.0f);
+  const float gl = readlane_f32(x.gam, 63);
+  const float end = lane < n ? x.end : 0.0f;
+  float f[2][8];
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[kb][e] = __shfl(end, 32 * kb + 8 * g + e);
+#pragma unroll
+  for (int nj = 0; nj < NJ; ++nj) {
+    const Split3 v0 = scaled_values(vr[0][nj], f[0]), v1 = scaled_values(vr[1][nj], f[1]);
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) {
+      v4f acc = S.s[ni][nj] * gl;
+      acc = mma3(ld_tokens<DK + 8>(kl, 0, 16 * ni), v0, acc);
+      acc = mma3(ld_tokens<DK + 8>(kl, 32, 16 * ni), v1, acc);
+      *reinterpret_cast<v4f *>(ck + LinState<DK, DV>::at(ni, nj)) = acc;
+    }
+  }
+}
+
+// D(t, s) of tile (st, tt) for token t = lane's m and s = 4 g + e of their blocks.
+__device__ __forceinline__ void tile_decay(const ChunkDecay &d, int st, int tt, float (&D)[4]) {
+  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+  const float at = d.al[kLB * tt + m];
+  if (st == tt) {
+    // the product after 4 g + 3 by a scan, then one factor more per step down
+    const float4 as = *reinterpret_cast<const float4 *>(d.al + kLB * st + 4 * g);
+    float x = row_prefix(m > 4 * g + 3 ? at : 1.0f);
+    D[3] = x;
+    x *= m >= 4 * g + 3 ? as.w : 1.0f;
+    D[2] = x;
+    x *= m >= 4 * g + 2 ? as.z : 1.0f;
+    D[1] = x;
+    x *= m >= 4 * g + 1 ? as.y : 1.0f;
+    D[0] = x;
+  } else {
+    float x = row_prefix(at);
+    for (int o = st + 1; o < tt; ++o) x *= d.al[kLB * o] * d.suf[kLB * o];
+    const float4 sf = *reinterpret_cast<const float4 *>(d.suf + kLB * st + 4 * g);
+    D[0] = x * sf.x;
+    D[1] = x * sf.y;
+    D[2] = x * sf.z;
+    D[3] = x * sf.w;
+  }
+}
+
+// ---- the state sum of every segment that another one follows ----
+template <int DK, int DV>
+__global__ __launch_bounds__(kLinThreads, 2) void lin_sum_kernel(LinArgs a) {
+  __shared__ __align__(16) uint16_t kl[kLinChunk * (DK + 8)];
+  __shared__ __align__(16) uint16_t vl[kLinChunk * (DV + 8)];
+  __shared__ __align__(16) ChunkDecay dec[2];
+  int unit, h;
+  LinRow r;
+  if (!lin_unit_head(a, unit, h) || !lin_find(a, true, unit, r) || r.err) return;
+  const int seg = unit - r.unit0;
+  if (seg + 1 >= r.nseg) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int64_t tok0 = (int64_t)r.c0 + (int64_t)seg * a.seg * kLinChunk;
+  const uint16_t *k = a.k + tok0 * a.ks + (int64_t)(h / a.group) * DK;
+  const uint16_t *v = a.v + tok0 * a.vs + (int64_t)h * DV;
+  const float *al = a.alpha + tok0 * a.as + h;
+
+  // every chunk of a segment that another follows is full
+  LinState<DK, DV> S;
+  S.zero();
+  float total = 1.0f;
+  Staged16<DK> ks;
+  Staged16<DV> vs;
+  ks.load(k, a.ks, kLinChunk);
+  vs.load(v, a.vs, kLinChunk);
+  float an = wave == 3 ? al[lane * a.as] : 0.0f;
+  if (wave == 3) put_chunk_decay(dec[0], an);
+  for (int c = 0; c < a.seg; ++c) {
+    __syncthreads();
+    ks.store(kl);
+    vs.store(vl);
+    __syncthreads();
+    const int64_t next = (int64_t)(c + 1) * kLinChunk;
+    if (c + 1 < a.seg) {
+      ks.load(k + next * a.ks, a.ks, kLinChunk);
+      vs.load(v + next * a.vs, a.vs, kLinChunk);
+      if (wave == 3) an = al[(next + lane) * a.as];
+    }
+    bf16x8 vr[2][DV / 64];
+    load_values<DV>(vl, vr);
+    chunk_state<DK, DV>(S, kl, vr, dec[c & 1]);
+    total *= dec[c & 1].gam[kLinChunk - 1];
+    if (wave == 3 && c + 1 < a.seg) put_chunk_decay(dec[(c + 1) & 1], an);
+  }
+  const int64_t sh = (int64_t)(r.slot0 + seg) * a.H + h;
+  S.store(a.ws + sh * (DK * DV), true);
+  if (threadIdx.x == 0) a.wdec[sh] = total;
+}
+
+// ---- the state entering every segment of a row, in place of the sums ----
+template <int DK, int DV>
+__global__ __launch_bounds__(kLinThreads) void lin_scan_kernel(LinArgs a) {
+  constexpr int PARTS = DK * DV / 4 / kLinThreads, NJ = DV / 64;
+  int bh, part, b, h;
+  divmod_uniform(blockIdx.x, PARTS, bh, part);
+  divmod_uniform(bh, a.H, b, h);
+  LinRow r;
+  if (!lin_find(a, false, b, r) || r.err || r.nseg < 2) return;
+  const int ni = part / NJ, nj = part % NJ;
+  v4f s = *reinterpret_cast<const v4f *>(a.cache + (int64_t)r.slot * a.slot_stride + (int64_t)h * (DK * DV) +
+                                         LinState<DK, DV>::at(ni, nj));
+  float *w = a.ws + ((int64_t)r.slot0 * a.H + h) * (DK * DV) + LinState<DK, DV>::ws_at(ni, nj);
+  const float *dec = a.wdec + (int64_t)r.slot0 * a.H + h;
+  const int64_t step = (int64_t)a.H * (DK * DV);
+  for (int j = 0; j + 1 < r.nseg; ++j) {
+    const v4f d = *reinterpret_cast<const v4f *>(w);
+    *reinterpret_cast<v4f *>(w) = s;
+    s = s * dec[(int64_t)j * a.H] + d;
+    w += step;
+  }
+  *reinterpret_cast<v4f *>(w) = s;
+}
+
+// ---- outputs, final state and checkpoint ----
+template <int DK, int DV, bool BF16>
+__global__ __launch_bounds__(kLinThreads, 2) void lin_out_kernel(LinArgs a) {
+  constexpr int NJ = DV / 64, KB = DK / 32, T = kLinChunk / kLB;
+  __shared__ __align__(16) uint16_t ql[kLinChunk * (DK + 8)];
+  __shared__ __align__(16) uint16_t kl[kLinChunk * (DK + 8)];
+  __shared__ __align__(16) uint16_t vl[kLinChunk * (DV + 8)];
+  __shared__ __align__(16) uint16_t pl[3][kLinChunk * kLP];  // decayed scores, high, middle and low parts
+  __shared__ __align__(16) ChunkDecay dec[2];
+  int unit, h;
+  LinRow r;
+  if (!lin_unit_head(a, unit, h)) return;
+  const bool found = lin_find(a, true, unit, r);
+  if (unit + 1 == a.units && h == 0 && threadIdx.x == 0 && a.dev_err && found && r.unit0 + r.nseg <= a.units) {
+    // rows past the launched units (only with rows that overlap)
+    if (r.b + 1 < a.B) atomicOr(a.dev_err, KDA_DEVERR_SEQLEN);
+  }
+  if (!found) return;
+  if (r.err) {
+    if (r.err > 0 && unit == r.unit0 && h == 0 && threadIdx.x == 0 && a.dev_err) atomicOr(a.dev_err, r.err);
+    return;
+  }
+  const int seg = unit - r.unit0;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+  const int ck = a.ckpt_pos ? a.ckpt_pos[r.b] : -1;
+  float *slot = a.cache + (int64_t)r.slot * a.slot_stride + (int64_t)h * (DK * DV);
+  float *ckpt = ck >= 0 ? a.ckpt + ((int64_t)r.b * a.H + h) * (DK * DV) : nullptr;
+  if (r.n == 0 && ck != 0) return;
+  LinState<DK, DV> S;
+  if (r.nseg > 1)
+    S.load(a.ws + ((int64_t)(r.slot0 + seg) * a.H + h) * (DK * DV), true);
+  else
+    S.load(slot, false);
+  if (ck == 0 && seg == 0) S.store(ckpt, false);
+  if (r.n == 0) return;
+
+  const int first = seg * a.seg * kLinChunk;                  // tokens of the row before the segment
+  const int n = min(r.n - first, a.seg * kLinChunk);          // and in it
+  const int64_t tok0 = (int64_t)r.c0 + first;
+  const uint16_t *q = a.q + tok0 * a.qs + (int64_t)(h / a.group) * DK;
+  const uint16_t *k = a.k + tok0 * a.ks + (int64_t)(h / a.group) * DK;
+  const uint16_t *v = a.v + tok0 * a.vs + (int64_t)h * DV;
+  const float *al = a.alpha + tok0 * a.as + h;
+  // the tiles above the diagonal that a product over 32 tokens reads: (1, 0) and (3, 2)
+  for (int i = threadIdx.x; i < 3 * 2 * kLB * kLB / 4; i += kLinThreads) {
+    const int part = i >> 7, up = (i >> 6) & 1, t = (i >> 2) & 15, s = (i & 3) * 4;
+    *reinterpret_cast<u32x2 *>(&pl[part][(32 * up + t) * kLP + 32 * up + kLB + s]) = (u32x2){0u, 0u};
+  }
+  Staged16<DK> qs, ks;
+  Staged16<DV> vs;
+  qs.load(q, a.qs, n);
+  ks.load(k, a.ks, n);
+  vs.load(v, a.vs, n);
+  float an = 1.0f;
+  if (wave == 3) {
+    if (lane < n) an = al[lane * a.as];
+    put_chunk_decay(dec[0], an);
+  }
+  for (int t0 = 0, c = 0; t0 < n; t0 += kLinChunk, ++c) {
+    const int nt = min(n - t0, kLinChunk);  // tokens of the chunk
+    const int left = n - t0 - kLinChunk;    // and after it
+    const ChunkDecay &d = dec[c & 1];
+    __syncthreads();
+    qs.store(ql);
+    ks.store(kl);
+    vs.store(vl);
+    __syncthreads();
+    if (left > 0) {
+      const int64_t next = t0 + kLinChunk;
+      qs.load(q + next * a.qs, a.qs, left);
+      ks.load(k + next * a.ks, a.ks, left);
+      vs.load(v + next * a.vs, a.vs, left);
+      if (wave == 3) an = lane < left ? al[(next + lane) * a.as] : 1.0f;
+    }
+
+    // decayed scores, transposed tiles [s][t]: the ten on and below the diagonal over the waves
+    for (int i = wave; i < T * (T + 1) / 2; i += 4) {
+      const int tt = i >= 6 ? 3 : i >= 3 ? 2 : i >= 1 ? 1 : 0, st = i - tt * (tt + 1) / 2;
+      v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+        acc = mma(ld_run8(kl + (kLB * st + m) * (DK + 8) + 32 * kb + 8 * g),
+                  ld_run8(ql + (kLB * tt + m) * (DK + 8) + 32 * kb + 8 * g), acc);
+      float D[4], p[4];
+      tile_decay(d, st, tt, D);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[e] = st < tt || m >= 4 * g + e ? acc[e] * D[e] : 0.0f;
+      uint32_t w[6];
+      split3_words<4>(p, w);
+#pragma unroll
+      for (int x = 0; x < 3; ++x)
+        *reinterpret_cast<u32x2 *>(&pl[x][(kLB * tt + m) * kLP + kLB * st + 4 * g]) = (u32x2){w[2 * x], w[2 * x + 1]};
+    }
+
+    // outputs, transposed tiles [j][t]: Gamma_t S0^T q_t
+    v4f o[NJ][T];
+#pragma unroll
+    for (int nj = 0; nj < NJ; ++nj)
+#pragma unroll
+      for (int tt = 0; tt < T; ++tt) o[nj][tt] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      Split3 sp[NJ];
+#pragma unroll
+      for (int nj = 0; nj < NJ; ++nj) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = S.s[2 * kb + e / 4][nj][e % 4];
+        sp[nj] = split3(x);
+      }
+#pragma unroll
+      for (int tt = 0; tt < T; ++tt) {
+        const bf16x8 qv = ld_run4x2(ql + (kLB * tt + m) * (DK + 8) + 32 * kb + 4 * g);
+#pragma unroll
+        for (int nj = 0; nj < NJ; ++nj) o[nj][tt] = mma3(sp[nj], qv, o[nj][tt]);
+      }
+    }
+#pragma unroll
+    for (int tt = 0; tt < T; ++tt) {
+      const float gam = d.gam[kLB * tt + m];
+#pragma unroll
+      for (int nj = 0; nj < NJ; ++nj) o[nj][tt] *= gam;
+    }
+    if (wave == 3 && left > 0) put_chunk_decay(dec[(c + 1) & 1], an);
+    __syncthreads();
+
+    // and sum_s D(t, s) (k_s . q_t) v_s
+    bf16x8 vr[2][NJ];
+    load_values<DV>(vl, vr);
+#pragma unroll
+    for (int tt = 0; tt < T; ++tt) {
+#pragma unroll
+      for (int kb = 0; kb <= tt / 2; ++kb) {
+        const int at = (kLB * tt + m) * kLP + 32 * kb + 8 * g;
+        const Split3 p = {ld_run8(&pl[0][at]), ld_run8(&pl[1][at]), ld_run8(&pl[2][at])};
+#pragma unroll
+        for (int nj = 0; nj < NJ; ++nj) o[nj][tt] = mma3(vr[kb][nj], p, o[nj][tt]);
+      }
+    }
+#pragma unroll
+    for (int tt = 0; tt < T; ++tt) {
+      const int t = kLB * tt + m;
+      if (t < nt) {
+        const int64_t at = ((tok0 + t0 + t) * a.H + h) * DV + wave * (DV / 4) + 4 * g;
+#pragma unroll
+        for (int nj = 0; nj < NJ; ++nj) {
+          const v4f y = o[nj][tt];
+          if constexpr (BF16) {
+            const u32x2 w = {f32_to_bf16(y[0]) | (uint32_t)f32_to_bf16(y[1]) << 16,
+                             f32_to_bf16(y[2]) | (uint32_t)f32_to_bf16(y[3]) << 16};
+            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) + at + 16 * nj) = w;
+          } else {
+            *reinterpret_cast<v4f *>(static_cast<float *>(a.out) + at + 16 * nj) = y;
+          }
+        }
+      }
+    }
+
+    const int cut = ck - first - t0;  // tokens of the chunk before the checkpoint
+    if (cut > 0 && cut < nt) chunk_checkpoint<DK, DV>(S, kl, vr, d, cut, ckpt);
+    chunk_state<DK, DV>(S, kl, vr, d);
+    if (cut > 0 && cut == nt) S.store(ckpt, false);
+  }
+  if (seg + 1 == r.nseg) S.store(slot, false);
 }
 
 }  // namespace
@@ -161,8 +777,14 @@ const void *lin_decode_kernel_for(int dk, int C, bool gate, bool bf16) {
   return dk == 64 ? lin_decode_for<64>(C, gate, bf16) : dk == 128 ? lin_decode_for<128>(C, gate, bf16) : nullptr;
 }
 
-const void *lin_prefill_kernel_for(int dk) {
-  return dk == 64 ? (const void *)lin_prefill_kernel<64> : (const void *)lin_prefill_kernel<128>;
+#define KDA_LIN_DIMS(KERNEL, ...)                                                                             \
+  (dk == 64 ? dv == 64 ? (const void *)KERNEL<64, 64 __VA_ARGS__> : (const void *)KERNEL<64, 128 __VA_ARGS__>   \
+            : dv == 64 ? (const void *)KERNEL<128, 64 __VA_ARGS__> : (const void *)KERNEL<128, 128 __VA_ARGS__>)
+
+const void *lin_sum_kernel_for(int dk, int dv) { return KDA_LIN_DIMS(lin_sum_kernel); }
+const void *lin_scan_kernel_for(int dk, int dv) { return KDA_LIN_DIMS(lin_scan_kernel); }
+const void *lin_out_kernel_for(int dk, int dv, bool bf16) {
+  return bf16 ? KDA_LIN_DIMS(lin_out_kernel, , true) : KDA_LIN_DIMS(lin_out_kernel, , false);
 }
 
 }  // namespace kda

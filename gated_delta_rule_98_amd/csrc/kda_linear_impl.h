@@ -22,10 +22,23 @@ struct LinArgs {
   float eps;
   int32_t B, H, group, dv, n_tok, ntile;  // group = H / Hk heads share a key head
   int32_t out_bf16;
+  // prefill: segments of seg chunks; units = B + (segments past each row's first, at most)
+  int32_t seg, units;
+  float *ws;    // states, [2 (units - B)][H][dv dk]
+  float *wdec;  // decays over a segment, [2 (units - B)][H]
 };
 
 const void *lin_decode_kernel_for(int dk, int C, bool gate, bool bf16);
-const void *lin_prefill_kernel_for(int dk);
+
+constexpr int kLinChunk = 64;    // tokens per chunk of the prefill
+constexpr int kLinThreads = 256; // threads of each of its kernels
+// Kernel handles of the prefill: the state sums of the segments, the states
+// entering them, and the outputs.
+const void *lin_sum_kernel_for(int dk, int dv);
+const void *lin_scan_kernel_for(int dk, int dv);
+const void *lin_out_kernel_for(int dk, int dv, bool bf16);
+// Workgroups of the scan per (row, head).
+inline int lin_scan_parts(int dk, int dv) { return dk * dv / 4 / kLinThreads; }
 
 // Arguments of the block norm.
 struct NormArgs {
