@@ -677,6 +677,7 @@ static int check_lin_tokens(const kda_lin_tokens *x, int32_t H, int32_t dk, int3
   const int64_t kw = (int64_t)x->Hk * dk, vw = (int64_t)H * dv;
   if (x->q_stride < kw || x->k_stride < kw || x->v_stride < vw) return KDA_ERR_INVALID;
   if (x->alpha_stride != 0 && x->alpha_stride < H) return KDA_ERR_INVALID;
+  if (std::max({x->q_stride, x->k_stride, x->v_stride, x->alpha_stride, vw}) > kLinMaxStride) return KDA_ERR_UNSUPPORTED;
   if (!aligned(x->q, 16) || !aligned(x->k, 16) || !aligned(x->v, 16) || !aligned(x->alpha, 4) ||
       x->q_stride % 8 != 0 || x->k_stride % 8 != 0 || x->v_stride % 8 != 0)
     return KDA_ERR_ALIGN;
@@ -837,13 +838,16 @@ int kda_lin_prefill(float *cache, int64_t num_slots, int64_t slot_stride, const 
   a.ws = static_cast<float *>(workspace);
   a.wdec = reinterpret_cast<float *>(static_cast<char *>(workspace) + lin_ws_state_bytes(s, H, dk, dv));
   if (n_tok == 0) a.group = 1;  // no tokens, no key heads
-  // units x key heads dealt to the 8 XCDs, the heads of a key head together
-  const int64_t blocks = (units * (H / a.group) + 7) / 8 * 8 * a.group;
+  // a unit's heads on one XCD, or over several where there are fewer units than XCDs
+  const int32_t hk = H / a.group;
+  a.piece_heads = units >= 8 ? H : (int32_t)((hk * units + 7) / 8) * a.group;
+  a.pieces = (H + a.piece_heads - 1) / a.piece_heads;
+  const int64_t blocks = (units * a.pieces + 7) / 8 * 8 * a.piece_heads;
   if (s.more > 0) {
-    KDA_TRY(launch_lin(lin_sum_kernel_for(dk, dv), blocks, kLinThreads, a, stream));
-    KDA_TRY(launch_lin(lin_scan_kernel_for(dk, dv), (int64_t)B * H * lin_scan_parts(dk, dv), kLinThreads, a, stream));
+    KDA_TRY(launch_lin(lin_sum_kernel_for(dk, dv), blocks, lin_threads(dv), a, stream));
+    KDA_TRY(launch_lin(lin_scan_kernel_for(dk, dv), (int64_t)B * H * lin_scan_parts(dk, dv), lin_threads(dv), a, stream));
   }
-  return launch_lin(lin_out_kernel_for(dk, dv, a.out_bf16), blocks, kLinThreads, a, stream);
+  return launch_lin(lin_out_kernel_for(dk, dv, a.out_bf16), blocks, lin_threads(dv), a, stream);
 }
 
 // ------------------------------------------------------------------ block norm

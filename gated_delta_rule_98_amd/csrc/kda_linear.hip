@@ -115,6 +115,9 @@ __global__ __launch_bounds__(GATE ? 1024 : 256) void lin_decode_kernel(LinArgs a
 // three bfloat16 parts, 8 + 8 + 8 bits of its 24, which is exact; the three
 // products are exact in fp32 and accumulate there.
 //
+// A checkpoint cuts its row's chunks: the one that reaches it ends there, so
+// the state there falls on a chunk's edge.
+//
 // Decay products never divide and never go through logarithms: a block of 16
 // tokens holds prefix products, suffix products and its own product, and D(t, s)
 // across blocks is prefix * (blocks between) * suffix. A product underflows
@@ -167,12 +170,13 @@ __device__ __forceinline__ v4f mma(bf16x8 a, bf16x8 b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// c + (hi + mid + lo) b and c + a (hi + mid + lo), small terms first
-__device__ __forceinline__ v4f mma3(const Split3 &a, bf16x8 b, v4f c) {
-  return mma(a.hi, b, mma(a.mid, b, mma(a.lo, b, c)));
-}
-__device__ __forceinline__ v4f mma3(bf16x8 a, const Split3 &b, v4f c) {
-  return mma(a, b.hi, mma(a, b.mid, mma(a, b.lo, c)));
+// x, computed anew wherever this stands: keeps the compiler from hoisting
+// 64-bit vector addresses out of the chunk loop (their registers would be
+// spilled, and a reload waits for every load in flight) in place of a scalar
+// base with a 32-bit offset.
+__device__ __forceinline__ uint32_t pinned(uint32_t x) {
+  asm volatile("" : "+v"(x));
+  return x;
 }
 
 // An MFMA operand whose contraction index runs over tokens, from a token-major
@@ -244,26 +248,17 @@ struct ChunkDecay {
 };
 
 // One wave, lane = token.
-struct LaneDecay {
-  float suf, gam, end;
-};
-__device__ __forceinline__ LaneDecay chunk_decay(float al) {
-  const int row = (threadIdx.x & 63) >> 4;
+__device__ __forceinline__ void put_chunk_decay(ChunkDecay &d, float al) {
+  const int lane = threadIdx.x & 63, row = lane >> 4;
   const double p = row_prefix((double)al), s = row_suffix((double)al);
   const double after = dpp_or_one<0x101>(s);  // the suffix of the next lane
   const double m0 = readlane_f64(p, 15), m1 = readlane_f64(p, 31), m2 = readlane_f64(p, 47), m3 = readlane_f64(p, 63);
   const double pre = row == 0 ? 1.0 : row == 1 ? m0 : row == 2 ? m0 * m1 : m0 * m1 * m2;
   const double post = row == 0 ? m1 * m2 * m3 : row == 1 ? m2 * m3 : row == 2 ? m3 : 1.0;
-  return {(float)after, (float)(p * pre), (float)(after * post)};
-}
-
-__device__ __forceinline__ void put_chunk_decay(ChunkDecay &d, float al) {
-  const int lane = threadIdx.x & 63;
-  const LaneDecay x = chunk_decay(al);
   d.al[lane] = al;
-  d.suf[lane] = x.suf;
-  d.gam[lane] = x.gam;
-  d.end[lane] = x.end;
+  d.suf[lane] = (float)after;
+  d.gam[lane] = (float)(p * pre);
+  d.end[lane] = (float)(after * post);
 }
 
 // One row's tokens and its place in the numbering of units: a row has
@@ -337,90 +332,84 @@ __device__ __forceinline__ bool lin_find(const LinArgs &a, bool by_unit, int key
   return false;
 }
 
-// Workgroups are dispatched round-robin over the 8 XCDs. The heads that share a
-// key head, in one unit, are one XCD's, next to each other in its order, so
-// that they read its q and k through one L2.
+// Workgroups are dispatched round-robin over the 8 XCDs. A unit's heads stand
+// side by side in memory, 256 bytes each of a token's row, so one XCD takes all
+// heads of a unit (or, with fewer units than XCDs, a run of its key heads):
+// its L2 channels, which interleave by address, then share the load, and q and
+// k of a shared key head are read once.
 __device__ __forceinline__ bool lin_unit_head(const LinArgs &a, int &unit, int &h) {
-  const int n = blockIdx.x, hk = a.H / a.group;
-  int j, in_group;
-  divmod_uniform(n >> 3, a.group, j, in_group);
-  const int g = 8 * j + (n & 7);
-  int kh;
-  divmod_uniform(g, hk, unit, kh);
-  h = kh * a.group + in_group;
-  return unit < a.units;
+  const int n = blockIdx.x, pieces = a.pieces, heads = a.piece_heads;
+  int j, in_piece, piece;
+  divmod_uniform(n >> 3, heads, j, in_piece);
+  divmod_uniform(8 * j + (n & 7), pieces, unit, piece);
+  h = piece * heads + in_piece;
+  return unit < a.units && h < a.H;
 }
 
-// Accumulator layout of a state. Wave w of the four holds value columns
-// [w DV/4, (w + 1) DV/4); its register tile [ni][nj] holds key channels
-// 16 ni + 4 g .. + 3 of column 16 nj + m in lane (m, g).
+// Accumulator layout of a state. Wave w holds value columns 16 w .. + 15; its
+// register tile ni holds key channels 16 ni + 4 g .. + 3 of column m in lane
+// (m, g).
 template <int DK, int DV>
 struct LinState {
-  static constexpr int NI = DK / 16, NJ = DV / 64;
-  v4f s[NI][NJ];
+  static constexpr int NI = DK / 16;
+  v4f s[NI];
 
-  __device__ static int64_t at(int ni, int nj) {  // element of a [dv][dk] state
+  __device__ static int at(int ni) {  // element of a [dv][dk] state
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    return (int64_t)(w * (DV / 4) + 16 * nj + (lane & 15)) * DK + 16 * ni + 4 * (lane >> 4);
+    return (16 * w + (lane & 15)) * DK + 16 * ni + 4 * (lane >> 4);
   }
-  __device__ static int ws_at(int ni, int nj) {  // element of a state in the workspace, in register order
-    return ((ni * NJ + nj) * kLinThreads + (int)threadIdx.x) * 4;
+  __device__ static int ws_at(int ni) {  // element of a state in the workspace, in register order
+    return (ni * lin_threads(DV) + (int)threadIdx.x) * 4;
   }
   __device__ __forceinline__ void load(const float *p, bool ws) {
 #pragma unroll
-    for (int ni = 0; ni < NI; ++ni)
-#pragma unroll
-      for (int nj = 0; nj < NJ; ++nj)
-        s[ni][nj] = *reinterpret_cast<const v4f *>(p + (ws ? (int64_t)ws_at(ni, nj) : at(ni, nj)));
+    for (int ni = 0; ni < NI; ++ni) s[ni] = *reinterpret_cast<const v4f *>(p + (ws ? ws_at(ni) : at(ni)));
   }
   __device__ __forceinline__ void store(float *p, bool ws) const {
 #pragma unroll
-    for (int ni = 0; ni < NI; ++ni)
-#pragma unroll
-      for (int nj = 0; nj < NJ; ++nj)
-        *reinterpret_cast<v4f *>(p + (ws ? (int64_t)ws_at(ni, nj) : at(ni, nj))) = s[ni][nj];
+    for (int ni = 0; ni < NI; ++ni) *reinterpret_cast<v4f *>(p + (ws ? ws_at(ni) : at(ni))) = s[ni];
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int ni = 0; ni < NI; ++ni)
-#pragma unroll
-      for (int nj = 0; nj < NJ; ++nj) s[ni][nj] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+    for (int ni = 0; ni < NI; ++ni) s[ni] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
   }
 };
 
-// A chunk of one token array on its way to LDS: 16-byte pieces, zero past the
-// chunk's n tokens.
-template <int D>
+// A chunk of one token array on its way to LDS, in 16-byte pieces. Offsets from
+// the chunk's first token fit 32 bits (strides are at most kLinMaxStride).
+// Tokens past the chunk's n are read from its last one (so that no load waits
+// behind a per-lane branch) and written as zeros.
+template <int D, int NT>
 struct Staged16 {
-  static constexpr int N = kLinChunk * D / 8 / kLinThreads, PITCH = D + 8;
-  uint4 x[N];
+  static constexpr int N = kLinChunk * D / 8 / NT, PITCH = D + 8, STEP = NT / (D / 8);
+  u32x4 x[N];
 
   __device__ __forceinline__ void load(const uint16_t *base, int64_t stride, int n) {
+    const int t = (int)threadIdx.x / (D / 8), c = ((int)threadIdx.x % (D / 8)) * 16;
+    const uint32_t st = 2 * (uint32_t)stride;  // bytes
+    if (n >= kLinChunk) {
+      const uint32_t off = pinned(t * st + c);
 #pragma unroll
-    for (int m = 0; m < N; ++m) {
-      const int p = (int)threadIdx.x + kLinThreads * m, t = p / (D / 8), c = (p % (D / 8)) * 8;
-      x[m] = make_uint4(0u, 0u, 0u, 0u);
-      if (t < n) x[m] = *reinterpret_cast<const uint4 *>(base + t * stride + c);
+      for (int m = 0; m < N; ++m) x[m] = *at(base + (int64_t)(STEP * m) * stride, off);
+    } else {
+#pragma unroll
+      for (int m = 0; m < N; ++m) x[m] = *at(base, pinned(min(t + STEP * m, n - 1) * st + c));
     }
   }
-  __device__ __forceinline__ void store(uint16_t *lds) const {
+  __device__ static const u32x4 *at(const uint16_t *base, uint32_t bytes) {
+    return reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(base) + bytes);
+  }
+  __device__ __forceinline__ void store(uint16_t *lds, int n) {
+    const int t = (int)threadIdx.x / (D / 8), c = ((int)threadIdx.x % (D / 8)) * 8;
+    if (n < kLinChunk) {
 #pragma unroll
-    for (int m = 0; m < N; ++m) {
-      const int p = (int)threadIdx.x + kLinThreads * m, t = p / (D / 8), c = (p % (D / 8)) * 8;
-      *reinterpret_cast<uint4 *>(lds + t * PITCH + c) = x[m];
+      for (int m = 0; m < N; ++m)
+        if (t + STEP * m >= n) x[m] = (u32x4){0u, 0u, 0u, 0u};
     }
+#pragma unroll
+    for (int m = 0; m < N; ++m) *reinterpret_cast<u32x4 *>(lds + (t + STEP * m) * PITCH + c) = x[m];
   }
 };
-
-// The wave's tokens of v: [kb][nj] holds tokens 32 kb + 8 g .. + 7 of column m.
-template <int DV>
-__device__ __forceinline__ void load_values(const uint16_t *vl, bf16x8 (&vr)[2][DV / 64]) {
-  const int w = threadIdx.x >> 6;
-#pragma unroll
-  for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-    for (int nj = 0; nj < DV / 64; ++nj) vr[kb][nj] = ld_tokens<DV + 8>(vl, 32 * kb, w * (DV / 4) + 16 * nj);
-}
 
 // Tokens 32 kb + 8 g .. + 7 of a column, each times its factor f, split.
 __device__ __forceinline__ Split3 scaled_values(bf16x8 v, const float (&f)[8]) {
@@ -436,55 +425,30 @@ __device__ __forceinline__ Split3 scaled_values(bf16x8 v, const float (&f)[8]) {
 
 // S <- Gamma_L S + sum_s end_s k_s v_s^T
 template <int DK, int DV>
-__device__ __forceinline__ void chunk_state(LinState<DK, DV> &S, const uint16_t *kl, const bf16x8 (&vr)[2][DV / 64],
+__device__ __forceinline__ void chunk_state(LinState<DK, DV> &S, const uint16_t *kl, const bf16x8 (&vr)[2],
                                             const ChunkDecay &d) {
-  constexpr int NI = DK / 16, NJ = DV / 64;
+  constexpr int NI = DK / 16;
   const int g = (threadIdx.x & 63) >> 4;
   const float gl = d.gam[kLinChunk - 1];
 #pragma unroll
-  for (int ni = 0; ni < NI; ++ni)
-#pragma unroll
-    for (int nj = 0; nj < NJ; ++nj) S.s[ni][nj] *= gl;
+  for (int ni = 0; ni < NI; ++ni) S.s[ni] *= gl;
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb) {
     float f[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = d.end[32 * kb + 8 * g + e];
-    Split3 vs[NJ];
+    const Split3 vs = scaled_values(vr[kb], f);
 #pragma unroll
-    for (int nj = 0; nj < NJ; ++nj) vs[nj] = scaled_values(vr[kb][nj], f);
+    for (int n4 = 0; n4 < NI; n4 += 4) {
+      bf16x8 kt[4];
 #pragma unroll
-    for (int ni = 0; ni < NI; ++ni) {
-      const bf16x8 kt = ld_tokens<DK + 8>(kl, 32 * kb, 16 * ni);
+      for (int i = 0; i < 4; ++i) kt[i] = ld_tokens<DK + 8>(kl, 32 * kb, 16 * (n4 + i));
 #pragma unroll
-      for (int nj = 0; nj < NJ; ++nj) S.s[ni][nj] = mma3(kt, vs[nj], S.s[ni][nj]);
-    }
-  }
-}
-
-// The state after the first n tokens of a chunk (0 < n < 64), to ck ([dv][dk]).
-template <int DK, int DV>
-__device__ __forceinline__ void chunk_checkpoint(const LinState<DK, DV> &S, const uint16_t *kl,
-                                                 const bf16x8 (&vr)[2][DV / 64], const ChunkDecay &d, int n, float *ck) {
-  constexpr int NI = DK / 16, NJ = DV / 64;
-  const int lane = threadIdx.x & 63, g = lane >> 4;
-  const LaneDecay x = chunk_decay(lane < n ? d.al[lane] : 1.0f);
-  const float gl = readlane_f32(x.gam, 63);
-  const float end = lane < n ? x.end : 0.0f;
-  float f[2][8];
+      for (int i = 0; i < 4; ++i) S.s[n4 + i] = mma(kt[i], vs.lo, S.s[n4 + i]);
 #pragma unroll
-  for (int kb = 0; kb < 2; ++kb)
+      for (int i = 0; i < 4; ++i) S.s[n4 + i] = mma(kt[i], vs.mid, S.s[n4 + i]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[kb][e] = __shfl(end, 32 * kb + 8 * g + e);
-#pragma unroll
-  for (int nj = 0; nj < NJ; ++nj) {
-    const Split3 v0 = scaled_values(vr[0][nj], f[0]), v1 = scaled_values(vr[1][nj], f[1]);
-#pragma unroll
-    for (int ni = 0; ni < NI; ++ni) {
-      v4f acc = S.s[ni][nj] * gl;
-      acc = mma3(ld_tokens<DK + 8>(kl, 0, 16 * ni), v0, acc);
-      acc = mma3(ld_tokens<DK + 8>(kl, 32, 16 * ni), v1, acc);
-      *reinterpret_cast<v4f *>(ck + LinState<DK, DV>::at(ni, nj)) = acc;
+      for (int i = 0; i < 4; ++i) S.s[n4 + i] = mma(kt[i], vs.hi, S.s[n4 + i]);
     }
   }
 }
@@ -517,7 +481,8 @@ __device__ __forceinline__ void tile_decay(const ChunkDecay &d, int st, int tt, 
 
 // ---- the state sum of every segment that another one follows ----
 template <int DK, int DV>
-__global__ __launch_bounds__(kLinThreads, 2) void lin_sum_kernel(LinArgs a) {
+__global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_sum_kernel(LinArgs a) {
+  constexpr int NT = lin_threads(DV), LAST = NT / 64 - 1;
   __shared__ __align__(16) uint16_t kl[kLinChunk * (DK + 8)];
   __shared__ __align__(16) uint16_t vl[kLinChunk * (DV + 8)];
   __shared__ __align__(16) ChunkDecay dec[2];
@@ -536,28 +501,28 @@ __global__ __launch_bounds__(kLinThreads, 2) void lin_sum_kernel(LinArgs a) {
   LinState<DK, DV> S;
   S.zero();
   float total = 1.0f;
-  Staged16<DK> ks;
-  Staged16<DV> vs;
+  Staged16<DK, NT> ks;
+  Staged16<DV, NT> vs;
   ks.load(k, a.ks, kLinChunk);
   vs.load(v, a.vs, kLinChunk);
-  float an = wave == 3 ? al[lane * a.as] : 0.0f;
-  if (wave == 3) put_chunk_decay(dec[0], an);
+  float an = 1.0f;
+  if (wave == LAST) put_chunk_decay(dec[0], al[lane * a.as]);
   for (int c = 0; c < a.seg; ++c) {
     __syncthreads();
-    ks.store(kl);
-    vs.store(vl);
+    ks.store(kl, kLinChunk);
+    vs.store(vl, kLinChunk);
     __syncthreads();
-    const int64_t next = (int64_t)(c + 1) * kLinChunk;
     if (c + 1 < a.seg) {
+      const int64_t next = (int64_t)(c + 1) * kLinChunk;
+      if (wave == LAST) an = al[(next + lane) * a.as];  // first: waited for during this chunk
+      __builtin_amdgcn_sched_barrier(0);
       ks.load(k + next * a.ks, a.ks, kLinChunk);
       vs.load(v + next * a.vs, a.vs, kLinChunk);
-      if (wave == 3) an = al[(next + lane) * a.as];
     }
-    bf16x8 vr[2][DV / 64];
-    load_values<DV>(vl, vr);
+    const bf16x8 vr[2] = {ld_tokens<DV + 8>(vl, 0, 16 * wave), ld_tokens<DV + 8>(vl, 32, 16 * wave)};
     chunk_state<DK, DV>(S, kl, vr, dec[c & 1]);
     total *= dec[c & 1].gam[kLinChunk - 1];
-    if (wave == 3 && c + 1 < a.seg) put_chunk_decay(dec[(c + 1) & 1], an);
+    if (wave == LAST && c + 1 < a.seg) put_chunk_decay(dec[(c + 1) & 1], an);
   }
   const int64_t sh = (int64_t)(r.slot0 + seg) * a.H + h;
   S.store(a.ws + sh * (DK * DV), true);
@@ -566,17 +531,15 @@ __global__ __launch_bounds__(kLinThreads, 2) void lin_sum_kernel(LinArgs a) {
 
 // ---- the state entering every segment of a row, in place of the sums ----
 template <int DK, int DV>
-__global__ __launch_bounds__(kLinThreads) void lin_scan_kernel(LinArgs a) {
-  constexpr int PARTS = DK * DV / 4 / kLinThreads, NJ = DV / 64;
-  int bh, part, b, h;
-  divmod_uniform(blockIdx.x, PARTS, bh, part);
+__global__ __launch_bounds__(lin_threads(DV)) void lin_scan_kernel(LinArgs a) {
+  int bh, ni, b, h;
+  divmod_uniform(blockIdx.x, lin_scan_parts(DK, DV), bh, ni);
   divmod_uniform(bh, a.H, b, h);
   LinRow r;
   if (!lin_find(a, false, b, r) || r.err || r.nseg < 2) return;
-  const int ni = part / NJ, nj = part % NJ;
   v4f s = *reinterpret_cast<const v4f *>(a.cache + (int64_t)r.slot * a.slot_stride + (int64_t)h * (DK * DV) +
-                                         LinState<DK, DV>::at(ni, nj));
-  float *w = a.ws + ((int64_t)r.slot0 * a.H + h) * (DK * DV) + LinState<DK, DV>::ws_at(ni, nj);
+                                         LinState<DK, DV>::at(ni));
+  float *w = a.ws + ((int64_t)r.slot0 * a.H + h) * (DK * DV) + LinState<DK, DV>::ws_at(ni);
   const float *dec = a.wdec + (int64_t)r.slot0 * a.H + h;
   const int64_t step = (int64_t)a.H * (DK * DV);
   for (int j = 0; j + 1 < r.nseg; ++j) {
@@ -590,8 +553,8 @@ __global__ __launch_bounds__(kLinThreads) void lin_scan_kernel(LinArgs a) {
 
 // ---- outputs, final state and checkpoint ----
 template <int DK, int DV, bool BF16>
-__global__ __launch_bounds__(kLinThreads, 2) void lin_out_kernel(LinArgs a) {
-  constexpr int NJ = DV / 64, KB = DK / 32, T = kLinChunk / kLB;
+__global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(LinArgs a) {
+  constexpr int NT = lin_threads(DV), NW = NT / 64, KB = DK / 32, T = kLinChunk / kLB;
   __shared__ __align__(16) uint16_t ql[kLinChunk * (DK + 8)];
   __shared__ __align__(16) uint16_t kl[kLinChunk * (DK + 8)];
   __shared__ __align__(16) uint16_t vl[kLinChunk * (DV + 8)];
@@ -601,11 +564,9 @@ __global__ __launch_bounds__(kLinThreads, 2) void lin_out_kernel(LinArgs a) {
   LinRow r;
   if (!lin_unit_head(a, unit, h)) return;
   const bool found = lin_find(a, true, unit, r);
-  if (unit + 1 == a.units && h == 0 && threadIdx.x == 0 && a.dev_err && found && r.unit0 + r.nseg <= a.units) {
-    // rows past the launched units (only with rows that overlap)
-    if (r.b + 1 < a.B) atomicOr(a.dev_err, KDA_DEVERR_SEQLEN);
-  }
   if (!found) return;
+  if (unit + 1 == a.units && r.b + 1 < a.B && r.unit0 + r.nseg <= a.units && h == 0 && threadIdx.x == 0 && a.dev_err)
+    atomicOr(a.dev_err, KDA_DEVERR_SEQLEN);  // rows past the launched units (only with rows that overlap)
   if (r.err) {
     if (r.err > 0 && unit == r.unit0 && h == 0 && threadIdx.x == 0 && a.dev_err) atomicOr(a.dev_err, r.err);
     return;
@@ -624,47 +585,49 @@ __global__ __launch_bounds__(kLinThreads, 2) void lin_out_kernel(LinArgs a) {
   if (ck == 0 && seg == 0) S.store(ckpt, false);
   if (r.n == 0) return;
 
-  const int first = seg * a.seg * kLinChunk;                  // tokens of the row before the segment
-  const int n = min(r.n - first, a.seg * kLinChunk);          // and in it
+  const int first = seg * a.seg * kLinChunk;          // tokens of the row before the segment
+  const int n = min(r.n - first, a.seg * kLinChunk);  // and in it
   const int64_t tok0 = (int64_t)r.c0 + first;
   const uint16_t *q = a.q + tok0 * a.qs + (int64_t)(h / a.group) * DK;
   const uint16_t *k = a.k + tok0 * a.ks + (int64_t)(h / a.group) * DK;
   const uint16_t *v = a.v + tok0 * a.vs + (int64_t)h * DV;
   const float *al = a.alpha + tok0 * a.as + h;
   // the tiles above the diagonal that a product over 32 tokens reads: (1, 0) and (3, 2)
-  for (int i = threadIdx.x; i < 3 * 2 * kLB * kLB / 4; i += kLinThreads) {
+  for (int i = threadIdx.x; i < 3 * 2 * kLB * kLB / 4; i += NT) {
     const int part = i >> 7, up = (i >> 6) & 1, t = (i >> 2) & 15, s = (i & 3) * 4;
     *reinterpret_cast<u32x2 *>(&pl[part][(32 * up + t) * kLP + 32 * up + kLB + s]) = (u32x2){0u, 0u};
   }
-  Staged16<DK> qs, ks;
-  Staged16<DV> vs;
-  qs.load(q, a.qs, n);
-  ks.load(k, a.ks, n);
-  vs.load(v, a.vs, n);
+  // chunks of up to 64 tokens, the one that reaches the checkpoint ends there
+  const int cut = ck - first;
+  const auto chunk_len = [&](int t0) { return min(kLinChunk, (t0 < cut ? min(cut, n) : n) - t0); };
+  Staged16<DK, NT> qs, ks;
+  Staged16<DV, NT> vs;
+  int nt = chunk_len(0);
+  qs.load(q, a.qs, nt);
+  ks.load(k, a.ks, nt);
+  vs.load(v, a.vs, nt);
   float an = 1.0f;
-  if (wave == 3) {
-    if (lane < n) an = al[lane * a.as];
-    put_chunk_decay(dec[0], an);
-  }
-  for (int t0 = 0, c = 0; t0 < n; t0 += kLinChunk, ++c) {
-    const int nt = min(n - t0, kLinChunk);  // tokens of the chunk
-    const int left = n - t0 - kLinChunk;    // and after it
+  if (wave == NW - 1) put_chunk_decay(dec[0], lane < nt ? al[lane * a.as] : 1.0f);
+  for (int t0 = 0, c = 0, next_nt; t0 < n; t0 += nt, nt = next_nt, ++c) {
+    const int next = t0 + nt;
+    next_nt = chunk_len(next);  // 0 past the last chunk
     const ChunkDecay &d = dec[c & 1];
     __syncthreads();
-    qs.store(ql);
-    ks.store(kl);
-    vs.store(vl);
+    qs.store(ql, nt);
+    ks.store(kl, nt);
+    vs.store(vl, nt);
     __syncthreads();
-    if (left > 0) {
-      const int64_t next = t0 + kLinChunk;
-      qs.load(q + next * a.qs, a.qs, left);
-      ks.load(k + next * a.ks, a.ks, left);
-      vs.load(v + next * a.vs, a.vs, left);
-      if (wave == 3) an = lane < left ? al[(next + lane) * a.as] : 1.0f;
+    if (next_nt > 0) {
+      // the decays first: they are waited for during this chunk
+      if (wave == NW - 1) an = lane < next_nt ? al[(int64_t)(next + lane) * a.as] : 1.0f;
+      __builtin_amdgcn_sched_barrier(0);
+      qs.load(q + (int64_t)next * a.qs, a.qs, next_nt);
+      ks.load(k + (int64_t)next * a.ks, a.ks, next_nt);
+      vs.load(v + (int64_t)next * a.vs, a.vs, next_nt);
     }
 
     // decayed scores, transposed tiles [s][t]: the ten on and below the diagonal over the waves
-    for (int i = wave; i < T * (T + 1) / 2; i += 4) {
+    for (int i = wave; i < T * (T + 1) / 2; i += NW) {
       const int tt = i >= 6 ? 3 : i >= 3 ? 2 : i >= 1 ? 1 : 0, st = i - tt * (tt + 1) / 2;
       v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -683,73 +646,65 @@ __global__ __launch_bounds__(kLinThreads, 2) void lin_out_kernel(LinArgs a) {
     }
 
     // outputs, transposed tiles [j][t]: Gamma_t S0^T q_t
-    v4f o[NJ][T];
+    v4f o[T];
 #pragma unroll
-    for (int nj = 0; nj < NJ; ++nj)
-#pragma unroll
-      for (int tt = 0; tt < T; ++tt) o[nj][tt] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+    for (int tt = 0; tt < T; ++tt) o[tt] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
-      Split3 sp[NJ];
+      float x[8];
 #pragma unroll
-      for (int nj = 0; nj < NJ; ++nj) {
-        float x[8];
+      for (int e = 0; e < 8; ++e) x[e] = S.s[2 * kb + e / 4][e % 4];
+      const Split3 sp = split3(x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = S.s[2 * kb + e / 4][nj][e % 4];
-        sp[nj] = split3(x);
-      }
-#pragma unroll
-      for (int tt = 0; tt < T; ++tt) {
-        const bf16x8 qv = ld_run4x2(ql + (kLB * tt + m) * (DK + 8) + 32 * kb + 4 * g);
-#pragma unroll
-        for (int nj = 0; nj < NJ; ++nj) o[nj][tt] = mma3(sp[nj], qv, o[nj][tt]);
+      for (int t2 = 0; t2 < T; t2 += 2) {
+        const bf16x8 q0 = ld_run4x2(ql + (kLB * t2 + m) * (DK + 8) + 32 * kb + 4 * g);
+        const bf16x8 q1 = ld_run4x2(ql + (kLB * (t2 + 1) + m) * (DK + 8) + 32 * kb + 4 * g);
+        o[t2] = mma(sp.lo, q0, o[t2]);
+        o[t2 + 1] = mma(sp.lo, q1, o[t2 + 1]);
+        o[t2] = mma(sp.mid, q0, o[t2]);
+        o[t2 + 1] = mma(sp.mid, q1, o[t2 + 1]);
+        o[t2] = mma(sp.hi, q0, o[t2]);
+        o[t2 + 1] = mma(sp.hi, q1, o[t2 + 1]);
       }
     }
 #pragma unroll
-    for (int tt = 0; tt < T; ++tt) {
-      const float gam = d.gam[kLB * tt + m];
-#pragma unroll
-      for (int nj = 0; nj < NJ; ++nj) o[nj][tt] *= gam;
-    }
-    if (wave == 3 && left > 0) put_chunk_decay(dec[(c + 1) & 1], an);
+    for (int tt = 0; tt < T; ++tt) o[tt] *= d.gam[kLB * tt + m];
+    if (wave == NW - 1 && next_nt > 0) put_chunk_decay(dec[(c + 1) & 1], an);
     __syncthreads();
 
     // and sum_s D(t, s) (k_s . q_t) v_s
-    bf16x8 vr[2][NJ];
-    load_values<DV>(vl, vr);
+    const bf16x8 vr[2] = {ld_tokens<DV + 8>(vl, 0, 16 * wave), ld_tokens<DV + 8>(vl, 32, 16 * wave)};
 #pragma unroll
-    for (int tt = 0; tt < T; ++tt) {
+    for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-      for (int kb = 0; kb <= tt / 2; ++kb) {
-        const int at = (kLB * tt + m) * kLP + 32 * kb + 8 * g;
-        const Split3 p = {ld_run8(&pl[0][at]), ld_run8(&pl[1][at]), ld_run8(&pl[2][at])};
+      for (int x = 2; x >= 0; --x)
 #pragma unroll
-        for (int nj = 0; nj < NJ; ++nj) o[nj][tt] = mma3(vr[kb][nj], p, o[nj][tt]);
+        for (int tt = 2 * kb; tt < T; ++tt)
+          o[tt] = mma(vr[kb], ld_run8(&pl[x][(kLB * tt + m) * kLP + 32 * kb + 8 * g]), o[tt]);
+    const int64_t orow = (int64_t)a.H * DV;
+    const int64_t obase = (tok0 + t0) * orow + (int64_t)h * DV + 16 * wave;
+    constexpr int OB = BF16 ? 2 : 4;  // bytes of an output
+    const uint32_t ooff = pinned(OB * (m * (uint32_t)orow + 4 * g));
+    const auto put = [&](int tt) {
+      char *to = static_cast<char *>(a.out) + OB * (obase + kLB * tt * orow) + ooff;
+      if constexpr (BF16) {
+        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+        *reinterpret_cast<bf16x4 *>(to) = __builtin_convertvector(o[tt], bf16x4);
+      } else {
+        *reinterpret_cast<v4f *>(to) = o[tt];
       }
-    }
+    };
+    if (nt == kLinChunk) {
 #pragma unroll
-    for (int tt = 0; tt < T; ++tt) {
-      const int t = kLB * tt + m;
-      if (t < nt) {
-        const int64_t at = ((tok0 + t0 + t) * a.H + h) * DV + wave * (DV / 4) + 4 * g;
+      for (int tt = 0; tt < T; ++tt) put(tt);
+    } else {
 #pragma unroll
-        for (int nj = 0; nj < NJ; ++nj) {
-          const v4f y = o[nj][tt];
-          if constexpr (BF16) {
-            const u32x2 w = {f32_to_bf16(y[0]) | (uint32_t)f32_to_bf16(y[1]) << 16,
-                             f32_to_bf16(y[2]) | (uint32_t)f32_to_bf16(y[3]) << 16};
-            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) + at + 16 * nj) = w;
-          } else {
-            *reinterpret_cast<v4f *>(static_cast<float *>(a.out) + at + 16 * nj) = y;
-          }
-        }
-      }
+      for (int tt = 0; tt < T; ++tt)
+        if (kLB * tt + m < nt) put(tt);
     }
 
-    const int cut = ck - first - t0;  // tokens of the chunk before the checkpoint
-    if (cut > 0 && cut < nt) chunk_checkpoint<DK, DV>(S, kl, vr, d, cut, ckpt);
     chunk_state<DK, DV>(S, kl, vr, d);
-    if (cut > 0 && cut == nt) S.store(ckpt, false);
+    if (next == cut) S.store(ckpt, false);
   }
   if (seg + 1 == r.nseg) S.store(slot, false);
 }

@@ -24,6 +24,7 @@ struct LinArgs {
   int32_t out_bf16;
   // prefill: segments of seg chunks; units = B + (segments past each row's first, at most)
   int32_t seg, units;
+  int32_t pieces, piece_heads;  // a unit's heads are dealt to the XCDs in `pieces` runs of piece_heads
   float *ws;    // states, [2 (units - B)][H][dv dk]
   float *wdec;  // decays over a segment, [2 (units - B)][H]
 };
@@ -31,14 +32,17 @@ struct LinArgs {
 const void *lin_decode_kernel_for(int dk, int C, bool gate, bool bf16);
 
 constexpr int kLinChunk = 64;    // tokens per chunk of the prefill
-constexpr int kLinThreads = 256; // threads of each of its kernels
+// Most elements between tokens: the bytes from a chunk's first token to its last fit 32 bits.
+constexpr int64_t kLinMaxStride = 1 << 24;
+// Threads of its kernels: a wave per 16 value columns.
+inline constexpr int lin_threads(int dv) { return 4 * dv; }
 // Kernel handles of the prefill: the state sums of the segments, the states
 // entering them, and the outputs.
 const void *lin_sum_kernel_for(int dk, int dv);
 const void *lin_scan_kernel_for(int dk, int dv);
 const void *lin_out_kernel_for(int dk, int dv, bool bf16);
 // Workgroups of the scan per (row, head).
-inline int lin_scan_parts(int dk, int dv) { return dk * dv / 4 / kLinThreads; }
+inline constexpr int lin_scan_parts(int dk, int dv) { return dk * dv / 4 / lin_threads(dv); }
 
 // Arguments of the block norm.
 struct NormArgs {

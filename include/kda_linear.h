@@ -47,7 +47,8 @@ extern "C" {
 /* Token inputs. Host struct; pointers are device memory. q, k and v are 16-byte
  * aligned with strides that are multiples of 8 (KDA_ERR_ALIGN), alpha is 4-byte
  * aligned. q_stride and k_stride are at least Hk * dk, v_stride at least H * dv,
- * alpha_stride 0 or at least H (KDA_ERR_INVALID). */
+ * alpha_stride 0 or at least H (KDA_ERR_INVALID); none of them, nor H * dv, is
+ * above 2^24 (KDA_ERR_UNSUPPORTED). */
 typedef struct kda_lin_tokens {
     const uint16_t *q, *k, *v;
     const float *alpha;

@@ -55,7 +55,8 @@ TOKEN_ERRORS = [
     (dict(vs=248), E.KDA_ERR_INVALID), (dict(as_=1), E.KDA_ERR_INVALID), (dict(as_=-2), E.KDA_ERR_INVALID),
     (dict(qs=260), E.KDA_ERR_ALIGN), (dict(ks=257), E.KDA_ERR_ALIGN), (dict(vs=258), E.KDA_ERR_ALIGN),
     (dict(q=A + 8), E.KDA_ERR_ALIGN), (dict(k=A + 2), E.KDA_ERR_ALIGN), (dict(v=A + 4), E.KDA_ERR_ALIGN),
-    (dict(alpha=A + 2), E.KDA_ERR_ALIGN)]
+    (dict(alpha=A + 2), E.KDA_ERR_ALIGN), (dict(qs=(1 << 24) + 8), E.KDA_ERR_UNSUPPORTED),
+    (dict(vs=(1 << 24) + 8), E.KDA_ERR_UNSUPPORTED), (dict(as_=(1 << 24) + 1), E.KDA_ERR_UNSUPPORTED)]
 
 
 @needs_no_gpu
