@@ -838,11 +838,7 @@ int kda_lin_prefill(float *cache, int64_t num_slots, int64_t slot_stride, const 
   a.ws = static_cast<float *>(workspace);
   a.wdec = reinterpret_cast<float *>(static_cast<char *>(workspace) + lin_ws_state_bytes(s, H, dk, dv));
   if (n_tok == 0) a.group = 1;  // no tokens, no key heads
-  // a unit's heads on one XCD, or over several where there are fewer units than XCDs
-  const int32_t hk = H / a.group;
-  a.piece_heads = units >= 8 ? H : (int32_t)((hk * units + 7) / 8) * a.group;
-  a.pieces = (H + a.piece_heads - 1) / a.piece_heads;
-  const int64_t blocks = (units * a.pieces + 7) / 8 * 8 * a.piece_heads;
+  const int64_t blocks = (units * (H / a.group) + 7) / 8 * 8 * a.group;
   if (s.more > 0) {
     KDA_TRY(launch_lin(lin_sum_kernel_for(dk, dv), blocks, lin_threads(dv), a, stream));
     KDA_TRY(launch_lin(lin_scan_kernel_for(dk, dv), (int64_t)B * H * lin_scan_parts(dk, dv), lin_threads(dv), a, stream));

@@ -126,7 +126,12 @@ __global__ __launch_bounds__(GATE ? 1024 : 256) void lin_decode_kernel(LinArgs a
 // formed in 64 bits and rounded once.
 
 constexpr int kLB = 16;                // block: the MFMA tile
-constexpr int kLP = kLinChunk + 8;     // row pitch of the scores, padded against bank conflicts
+// Decayed scores in LDS, [t][s] with s up to the end of t's half of the chunk:
+// rows of 32 and of 64, padded by 8 against bank conflicts.
+constexpr int kScoreElems = 32 * (32 + 8) + 32 * (64 + 8);
+__device__ __forceinline__ int score_row(int tt, int m) {  // element of row 16 tt + m
+  return tt < 2 ? (kLB * tt + m) * 40 : 32 * 40 + (kLB * (tt - 2) + m) * 72;
+}
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -290,9 +295,32 @@ __device__ __forceinline__ int lin_segments(const LinArgs &a, int n) {
   return chunks > a.seg ? (chunks + a.seg - 1) / a.seg : 1;
 }
 
+// Inclusive prefix sum over the wave: inside 16-lane rows, then the last lane
+// of each row (row_bcast:15) and of each half (row_bcast:31) to the rows after it.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int x) {
+  return x + __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_prefix_sum(int x) {
+  x = dpp_add<0x111, 0xF>(x);
+  x = dpp_add<0x112, 0xF>(x);
+  x = dpp_add<0x114, 0xF>(x);
+  x = dpp_add<0x118, 0xF>(x);
+  x = dpp_add<0x142, 0xA>(x);
+  return dpp_add<0x143, 0xC>(x);
+}
+
 // The row that holds a unit (by_unit) or the row of that number, found by each
 // wave over 64 rows at a time; false where there is none.
 __device__ __forceinline__ bool lin_find(const LinArgs &a, bool by_unit, int key, LinRow &r) {
+  if (a.units == a.B || a.B == 1) {  // no row is cut (unit = row) or there is only one: no search
+    r.b = a.B == 1 ? 0 : key;
+    r.unit0 = r.b;
+    r.slot0 = 0;
+    r.err = lin_row_check(a, r.b, r.slot, r.c0, r.n);
+    r.nseg = lin_segments(a, r.n);
+    return key < r.unit0 + r.nseg;
+  }
   const int lane = threadIdx.x & 63;
   int units = 0, slots = 0;
   for (int base = 0; base < a.B; base += 64) {
@@ -303,22 +331,16 @@ __device__ __forceinline__ bool lin_find(const LinArgs &a, bool by_unit, int key
       err = lin_row_check(a, b, slot, c0, n);
       nseg = lin_segments(a, n);
     }
-    int iu = nseg, is = nseg > 1 ? nseg : 0;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int u = __shfl_up(iu, d), s = __shfl_up(is, d);
-      if (lane >= d) {
-        iu += u;
-        is += s;
-      }
-    }
+    const int iu = wave_prefix_sum(nseg);
     const uint64_t hit = __ballot(b < a.B && (by_unit ? key < units + iu : b == key));
+    const uint64_t whole = __ballot(nseg == 1);  // rows without state slots
     if (hit) {
       const int l = __builtin_ctzll(hit);
       r.b = base + l;
       r.nseg = __builtin_amdgcn_readlane(nseg, l);
-      r.unit0 = units + __builtin_amdgcn_readlane(iu, l) - r.nseg;
-      r.slot0 = slots + __builtin_amdgcn_readlane(is, l) - (r.nseg > 1 ? r.nseg : 0);
+      const int before = __builtin_amdgcn_readlane(iu, l) - r.nseg;
+      r.unit0 = units + before;
+      r.slot0 = slots + before - __builtin_popcountll(whole & ((1ull << l) - 1));
       r.n = __builtin_amdgcn_readlane(n, l);
       r.c0 = __builtin_amdgcn_readlane(c0, l);
       r.slot = __builtin_amdgcn_readlane(slot, l);
@@ -326,24 +348,25 @@ __device__ __forceinline__ bool lin_find(const LinArgs &a, bool by_unit, int key
       if (r.err == 0 && r.unit0 + r.nseg > a.units) r.err = KDA_DEVERR_SEQLEN;
       return true;
     }
-    units += __builtin_amdgcn_readlane(iu, 63);
-    slots += __builtin_amdgcn_readlane(is, 63);
+    const int all = __builtin_amdgcn_readlane(iu, 63);
+    units += all;
+    slots += all - __builtin_popcountll(whole);
   }
   return false;
 }
 
-// Workgroups are dispatched round-robin over the 8 XCDs. A unit's heads stand
-// side by side in memory, 256 bytes each of a token's row, so one XCD takes all
-// heads of a unit (or, with fewer units than XCDs, a run of its key heads):
-// its L2 channels, which interleave by address, then share the load, and q and
-// k of a shared key head are read once.
+// Workgroups are dispatched round-robin over the 8 XCDs. The (unit, key head)
+// pairs are dealt to them in turn; the heads that share a key head stand next to
+// each other in one XCD's order, so that they read its q and k through one L2.
+// (Dealing whole units instead, so that a token's neighbouring heads meet in one
+// L2, measured the same on one long row and 15% slower on ragged ones.)
 __device__ __forceinline__ bool lin_unit_head(const LinArgs &a, int &unit, int &h) {
-  const int n = blockIdx.x, pieces = a.pieces, heads = a.piece_heads;
-  int j, in_piece, piece;
-  divmod_uniform(n >> 3, heads, j, in_piece);
-  divmod_uniform(8 * j + (n & 7), pieces, unit, piece);
-  h = piece * heads + in_piece;
-  return unit < a.units && h < a.H;
+  const int n = blockIdx.x, hk = a.H / a.group;
+  int j, in_group, kh;
+  divmod_uniform(n >> 3, a.group, j, in_group);
+  divmod_uniform(8 * j + (n & 7), hk, unit, kh);
+  h = kh * a.group + in_group;
+  return unit < a.units;
 }
 
 // Accumulator layout of a state. Wave w holds value columns 16 w .. + 15; its
@@ -453,6 +476,22 @@ __device__ __forceinline__ void chunk_state(LinState<DK, DV> &S, const uint16_t 
   }
 }
 
+// Chunks of a segment of n tokens with a checkpoint after cut of them: 64 tokens
+// each, the one that reaches a cut inside the segment ends there.
+struct LinChunks {
+  int n, cut, n1, count;  // n1: chunks before the cut
+
+  __device__ __forceinline__ LinChunks(int n_, int cut_) : n(n_), cut(cut_ > 0 && cut_ < n_ ? cut_ : n_) {
+    n1 = (cut + kLinChunk - 1) / kLinChunk;
+    count = n1 + (n - cut + kLinChunk - 1) / kLinChunk;
+  }
+  // tokens [t0, t0 + nt) of chunk c; nt = 0 past the last
+  __device__ __forceinline__ void at(int c, int &t0, int &nt) const {
+    t0 = c < n1 ? c * kLinChunk : cut + (c - n1) * kLinChunk;
+    nt = max(0, min(kLinChunk, (c < n1 ? cut : n) - t0));
+  }
+};
+
 // D(t, s) of tile (st, tt) for token t = lane's m and s = 4 g + e of their blocks.
 __device__ __forceinline__ void tile_decay(const ChunkDecay &d, int st, int tt, float (&D)[4]) {
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
@@ -482,10 +521,10 @@ __device__ __forceinline__ void tile_decay(const ChunkDecay &d, int st, int tt, 
 // ---- the state sum of every segment that another one follows ----
 template <int DK, int DV>
 __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_sum_kernel(LinArgs a) {
-  constexpr int NT = lin_threads(DV), LAST = NT / 64 - 1;
+  constexpr int NT = lin_threads(DV), NW = NT / 64;
   __shared__ __align__(16) uint16_t kl[kLinChunk * (DK + 8)];
   __shared__ __align__(16) uint16_t vl[kLinChunk * (DV + 8)];
-  __shared__ __align__(16) ChunkDecay dec[2];
+  __shared__ __align__(16) ChunkDecay dec[NW];
   int unit, h;
   LinRow r;
   if (!lin_unit_head(a, unit, h) || !lin_find(a, true, unit, r) || r.err) return;
@@ -497,32 +536,42 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_sum_kernel(L
   const uint16_t *v = a.v + tok0 * a.vs + (int64_t)h * DV;
   const float *al = a.alpha + tok0 * a.as + h;
 
-  // every chunk of a segment that another follows is full
+  // Every chunk of a segment that another follows is full. The chunk two ahead
+  // is requested while one is computed (two register sets rotate), and every NW
+  // chunks each wave forms the decays of one of the next NW.
   LinState<DK, DV> S;
   S.zero();
   float total = 1.0f;
-  Staged16<DK, NT> ks;
-  Staged16<DV, NT> vs;
-  ks.load(k, a.ks, kLinChunk);
-  vs.load(v, a.vs, kLinChunk);
-  float an = 1.0f;
-  if (wave == LAST) put_chunk_decay(dec[0], al[lane * a.as]);
-  for (int c = 0; c < a.seg; ++c) {
+  Staged16<DK, NT> ks[2];
+  Staged16<DV, NT> vs[2];
+  const auto load = [&](int c, int p) {
+    if (c >= a.seg) return;
+    const int64_t at = (int64_t)c * kLinChunk;
+    ks[p].load(k + at * a.ks, a.ks, kLinChunk);
+    vs[p].load(v + at * a.vs, a.vs, kLinChunk);
+  };
+  const auto load_decay = [&](int c) { return c < a.seg ? al[((int64_t)c * kLinChunk + lane) * a.as] : 1.0f; };
+  float an = load_decay(wave);
+  const auto step = [&](int c, int p) {
     __syncthreads();
-    ks.store(kl, kLinChunk);
-    vs.store(vl, kLinChunk);
-    __syncthreads();
-    if (c + 1 < a.seg) {
-      const int64_t next = (int64_t)(c + 1) * kLinChunk;
-      if (wave == LAST) an = al[(next + lane) * a.as];  // first: waited for during this chunk
-      __builtin_amdgcn_sched_barrier(0);
-      ks.load(k + next * a.ks, a.ks, kLinChunk);
-      vs.load(v + next * a.vs, a.vs, kLinChunk);
+    ks[p].store(kl, kLinChunk);
+    vs[p].store(vl, kLinChunk);
+    if (c % NW == 0) {
+      put_chunk_decay(dec[wave], an);
+      an = load_decay(c + NW + wave);
     }
+    __syncthreads();
+    load(c + 2, p);
     const bf16x8 vr[2] = {ld_tokens<DV + 8>(vl, 0, 16 * wave), ld_tokens<DV + 8>(vl, 32, 16 * wave)};
-    chunk_state<DK, DV>(S, kl, vr, dec[c & 1]);
-    total *= dec[c & 1].gam[kLinChunk - 1];
-    if (wave == LAST && c + 1 < a.seg) put_chunk_decay(dec[(c + 1) & 1], an);
+    const ChunkDecay &d = dec[c % NW];
+    chunk_state<DK, DV>(S, kl, vr, d);
+    total *= d.gam[kLinChunk - 1];
+  };
+  load(0, 0);
+  load(1, 1);
+  for (int c = 0; c < a.seg; c += 2) {
+    step(c, 0);
+    if (c + 1 < a.seg) step(c + 1, 1);
   }
   const int64_t sh = (int64_t)(r.slot0 + seg) * a.H + h;
   S.store(a.ws + sh * (DK * DV), true);
@@ -558,8 +607,8 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
   __shared__ __align__(16) uint16_t ql[kLinChunk * (DK + 8)];
   __shared__ __align__(16) uint16_t kl[kLinChunk * (DK + 8)];
   __shared__ __align__(16) uint16_t vl[kLinChunk * (DV + 8)];
-  __shared__ __align__(16) uint16_t pl[3][kLinChunk * kLP];  // decayed scores, high, middle and low parts
-  __shared__ __align__(16) ChunkDecay dec[2];
+  __shared__ __align__(16) uint16_t pl[3][kScoreElems];  // decayed scores, high, middle and low parts
+  __shared__ __align__(16) ChunkDecay dec[NW];  // of a group of NW chunks
   int unit, h;
   LinRow r;
   if (!lin_unit_head(a, unit, h)) return;
@@ -595,36 +644,40 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
   // the tiles above the diagonal that a product over 32 tokens reads: (1, 0) and (3, 2)
   for (int i = threadIdx.x; i < 3 * 2 * kLB * kLB / 4; i += NT) {
     const int part = i >> 7, up = (i >> 6) & 1, t = (i >> 2) & 15, s = (i & 3) * 4;
-    *reinterpret_cast<u32x2 *>(&pl[part][(32 * up + t) * kLP + 32 * up + kLB + s]) = (u32x2){0u, 0u};
+    *reinterpret_cast<u32x2 *>(&pl[part][score_row(2 * up, t) + 32 * up + kLB + s]) = (u32x2){0u, 0u};
   }
-  // chunks of up to 64 tokens, the one that reaches the checkpoint ends there
-  const int cut = ck - first;
-  const auto chunk_len = [&](int t0) { return min(kLinChunk, (t0 < cut ? min(cut, n) : n) - t0); };
+  const LinChunks chunks(n, ck - first);
   Staged16<DK, NT> qs, ks;
   Staged16<DV, NT> vs;
-  int nt = chunk_len(0);
-  qs.load(q, a.qs, nt);
-  ks.load(k, a.ks, nt);
-  vs.load(v, a.vs, nt);
-  float an = 1.0f;
-  if (wave == NW - 1) put_chunk_decay(dec[0], lane < nt ? al[lane * a.as] : 1.0f);
-  for (int t0 = 0, c = 0, next_nt; t0 < n; t0 += nt, nt = next_nt, ++c) {
-    const int next = t0 + nt;
-    next_nt = chunk_len(next);  // 0 past the last chunk
-    const ChunkDecay &d = dec[c & 1];
+  const auto load = [&](int c) {
+    int t0, nt;
+    chunks.at(c, t0, nt);
+    if (nt == 0) return;
+    qs.load(q + (int64_t)t0 * a.qs, a.qs, nt);
+    ks.load(k + (int64_t)t0 * a.ks, a.ks, nt);
+    vs.load(v + (int64_t)t0 * a.vs, a.vs, nt);
+  };
+  const auto load_decay = [&](int c) {
+    int t0, nt;
+    chunks.at(c, t0, nt);
+    return lane < nt ? al[(int64_t)(t0 + lane) * a.as] : 1.0f;
+  };
+  float an = load_decay(wave);
+  load(0);
+  for (int c = 0; c < chunks.count; ++c) {
+    int t0, nt;
+    chunks.at(c, t0, nt);
+    const ChunkDecay &d = dec[c % NW];
     __syncthreads();
+    if (c % NW == 0) {  // the decays of the next NW chunks, one per wave
+      put_chunk_decay(dec[wave], an);
+      an = load_decay(c + NW + wave);
+    }
     qs.store(ql, nt);
     ks.store(kl, nt);
     vs.store(vl, nt);
     __syncthreads();
-    if (next_nt > 0) {
-      // the decays first: they are waited for during this chunk
-      if (wave == NW - 1) an = lane < next_nt ? al[(int64_t)(next + lane) * a.as] : 1.0f;
-      __builtin_amdgcn_sched_barrier(0);
-      qs.load(q + (int64_t)next * a.qs, a.qs, next_nt);
-      ks.load(k + (int64_t)next * a.ks, a.ks, next_nt);
-      vs.load(v + (int64_t)next * a.vs, a.vs, next_nt);
-    }
+    load(c + 1);
 
     // decayed scores, transposed tiles [s][t]: the ten on and below the diagonal over the waves
     for (int i = wave; i < T * (T + 1) / 2; i += NW) {
@@ -642,7 +695,7 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
       split3_words<4>(p, w);
 #pragma unroll
       for (int x = 0; x < 3; ++x)
-        *reinterpret_cast<u32x2 *>(&pl[x][(kLB * tt + m) * kLP + kLB * st + 4 * g]) = (u32x2){w[2 * x], w[2 * x + 1]};
+        *reinterpret_cast<u32x2 *>(&pl[x][score_row(tt, m) + kLB * st + 4 * g]) = (u32x2){w[2 * x], w[2 * x + 1]};
     }
 
     // outputs, transposed tiles [j][t]: Gamma_t S0^T q_t
@@ -669,7 +722,6 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
     }
 #pragma unroll
     for (int tt = 0; tt < T; ++tt) o[tt] *= d.gam[kLB * tt + m];
-    if (wave == NW - 1 && next_nt > 0) put_chunk_decay(dec[(c + 1) & 1], an);
     __syncthreads();
 
     // and sum_s D(t, s) (k_s . q_t) v_s
@@ -680,7 +732,7 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
       for (int x = 2; x >= 0; --x)
 #pragma unroll
         for (int tt = 2 * kb; tt < T; ++tt)
-          o[tt] = mma(vr[kb], ld_run8(&pl[x][(kLB * tt + m) * kLP + 32 * kb + 8 * g]), o[tt]);
+          o[tt] = mma(vr[kb], ld_run8(&pl[x][score_row(tt, m) + 32 * kb + 8 * g]), o[tt]);
     const int64_t orow = (int64_t)a.H * DV;
     const int64_t obase = (tok0 + t0) * orow + (int64_t)h * DV + 16 * wave;
     constexpr int OB = BF16 ? 2 : 4;  // bytes of an output
@@ -704,7 +756,7 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
     }
 
     chunk_state<DK, DV>(S, kl, vr, d);
-    if (next == cut) S.store(ckpt, false);
+    if (first + t0 + nt == ck) S.store(ckpt, false);
   }
   if (seg + 1 == r.nseg) S.store(slot, false);
 }

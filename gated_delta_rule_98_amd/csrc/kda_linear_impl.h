@@ -24,7 +24,6 @@ struct LinArgs {
   int32_t out_bf16;
   // prefill: segments of seg chunks; units = B + (segments past each row's first, at most)
   int32_t seg, units;
-  int32_t pieces, piece_heads;  // a unit's heads are dealt to the XCDs in `pieces` runs of piece_heads
   float *ws;    // states, [2 (units - B)][H][dv dk]
   float *wdec;  // decays over a segment, [2 (units - B)][H]
 };
