@@ -11,6 +11,8 @@ tensors' device, or to ``stream``, whichever device is current.
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 from typing import Optional
 
 import torch
@@ -24,13 +26,18 @@ class kda_lin_tokens(ctypes.Structure):
                 ("v_stride", ctypes.c_int64), ("alpha_stride", ctypes.c_int64), ("Hk", ctypes.c_int32)]
 
 
+# The same layout, packed at a third of the cost of the ctypes structure: a small
+# call is bound by this binding, not by its kernel.
+_TOKENS = struct.Struct("@QQQQqqqqi4x")
+assert _TOKENS.size == ctypes.sizeof(kda_lin_tokens)
+
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _OUT = (torch.float32,) + _BF16_TYPES
 
 
-def _on(dev: int, t, name: str, dtypes, shape) -> int:
-    """Address of a contiguous tensor of the given types and shape on GPU ``dev``."""
+def _refuse(dev: int, t, name: str, dtypes, shape) -> None:
+    """Why tensor t is not one of the given types and shape on GPU ``dev``."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
@@ -39,6 +46,12 @@ def _on(dev: int, t, name: str, dtypes, shape) -> int:
         raise ValueError(f"{name} must be on GPU {dev}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _on(dev: int, t, name: str, dtypes, shape) -> int:
+    """Address of a contiguous tensor of the given types and shape on GPU ``dev``."""
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.get_device() == dev and t.shape == shape):
+        _refuse(dev, t, name, dtypes, shape)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -46,21 +59,17 @@ def _on(dev: int, t, name: str, dtypes, shape) -> int:
 
 def _heads(dev: int, t, name: str, rows: int, heads: int, d: int):
     """(address, stride between tokens) of a bf16 [rows, heads, d] tensor whose heads are contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _BF16_TYPES:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {_BF16_TYPES}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on GPU {dev}, got {t.device}")
-    if t.shape != (rows, heads, d):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, heads, d)}")
+    if not (isinstance(t, torch.Tensor) and t.dtype in _BF16_TYPES and t.get_device() == dev
+            and t.shape == (rows, heads, d)):
+        _refuse(dev, t, name, _BF16_TYPES, (rows, heads, d))
     s = t.stride()
-    if s[2] != 1 or (heads > 1 and s[1] != d):
+    if s[2] != 1 or (s[1] != d and heads > 1):
         raise ValueError(f"{name}: each token's heads must be contiguous, got strides {s}")
     return t.data_ptr(), (s[0] if rows > 1 else heads * d)
 
 
-def _tokens(dev: int, rows: int, H: int, dk: int, dv: int, q, k, v, alpha) -> kda_lin_tokens:
+def _tokens(dev: int, rows: int, H: int, dk: int, dv: int, q, k, v, alpha) -> bytes:
+    """The kda_lin_tokens of a call."""
     Hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
     if Hk < 1 or H % Hk:
         raise ValueError(f"k must be [rows, Hk, dk] with Hk dividing H = {H}")
@@ -68,15 +77,13 @@ def _tokens(dev: int, rows: int, H: int, dk: int, dv: int, q, k, v, alpha) -> kd
     kp, ks = _heads(dev, k, "k", rows, Hk, dk)
     vp, vs = _heads(dev, v, "v", rows, H, dv)
     if isinstance(alpha, torch.Tensor) and alpha.dim() == 1:
-        ap, astride = _on(dev, alpha, "alpha", _F32, (H,)), 0
-    else:
-        ap, astride = _on(dev, alpha, "alpha", _F32, (rows, H)), H
-    return kda_lin_tokens(qp, kp, vp, ap, qs, ks, vs, astride, Hk)
+        return _TOKENS.pack(qp, kp, vp, _on(dev, alpha, "alpha", _F32, (H,)), qs, ks, vs, 0, Hk)
+    return _TOKENS.pack(qp, kp, vp, _on(dev, alpha, "alpha", _F32, (rows, H)), qs, ks, vs, H, Hk)
 
 
 def _cache(cache):
     """cache: float32 [num_slots, H, dv, dk]; each slot contiguous, slots at stride(0)."""
-    if not isinstance(cache, torch.Tensor) or not cache.is_cuda or cache.dtype != torch.float32 or cache.dim() != 4:
+    if not isinstance(cache, torch.Tensor) or not cache.is_cuda or cache.dtype is not torch.float32 or cache.dim() != 4:
         raise ValueError("cache must be a float32 GPU tensor [num_slots, H, dv, dk]")
     ns, H, dv, dk = cache.shape
     s = cache.stride()
@@ -96,15 +103,25 @@ def _call(dev: int, fn, name: str, *args) -> None:
         raise KdaError(rc, name)
 
 
+# The current stream's handle without building a Stream object, where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _stream_of(dev: int, stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _raw_stream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_BF16_OUT = kda_options(0, 0, KDA_OUT_BF16)
 
 
 def _options(tile_w: int, out: torch.Tensor):
     bf16 = out.dtype is not torch.float32
-    return ctypes.byref(kda_options(int(tile_w), 0, KDA_OUT_BF16 if bf16 else 0)) if tile_w or bf16 else None
+    if tile_w:
+        return ctypes.byref(kda_options(int(tile_w), 0, KDA_OUT_BF16 if bf16 else 0))
+    return ctypes.byref(_BF16_OUT) if bf16 else None
 
 
 def kda_lin_decode_step(cache: torch.Tensor, slot_ids: torch.Tensor, q, k, v, alpha, out: torch.Tensor, *,
@@ -131,9 +148,10 @@ def kda_lin_decode_step(cache: torch.Tensor, slot_ids: torch.Tensor, q, k, v, al
         raise ValueError("weight needs a gate")
     err = None if dev_err is None else _on(dev, dev_err, "dev_err", _I32, dev_err.shape)
     _call(dev, load_library().kda_lin_decode_step, "kda_lin_decode_step", cache.data_ptr(), ns, stride, slots,
-          B, H, dk, dv, ctypes.byref(x), op, epi, err, _options(tile_w, out), _stream_of(dev, stream))
+          B, H, dk, dv, x, op, epi, err, _options(tile_w, out), _stream_of(dev, stream))
 
 
+@functools.lru_cache(maxsize=1024)
 def kda_lin_prefill_workspace(B: int, n_tok: int, H: int, dk: int, dv: int) -> int:
     """Workspace bytes kda_lin_prefill needs for these sizes (0: none)."""
     n = ctypes.c_size_t(0)
@@ -181,4 +199,4 @@ def kda_lin_prefill(cache: torch.Tensor, slot_ids: torch.Tensor, cu_seqlens: tor
             raise ValueError(f"workspace must be a contiguous tensor on GPU {dev}")
         ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _call(dev, load_library().kda_lin_prefill, "kda_lin_prefill", cache.data_ptr(), ns, stride, slots, cu, B,
-          n_tok, H, dk, dv, ctypes.byref(x), op, pos, ck, ws, nbytes, err, _options(0, out), handle)
+          n_tok, H, dk, dv, x, op, pos, ck, ws, nbytes, err, _options(0, out), handle)

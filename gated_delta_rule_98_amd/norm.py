@@ -12,7 +12,7 @@ from typing import Optional
 import torch
 
 from .kda import _BF16_TYPES, load_library
-from .linear import _F32, _OUT, _call, _on, _stream_of
+from .linear import _F32, _OUT, _call, _on, _refuse, _stream_of
 
 KDA_NORM_RESID_BF16 = 1
 KDA_NORM_Y_BF16 = 2
@@ -23,14 +23,8 @@ def _rows(dev: int, t, name: str, dtypes, rows: int, D: int):
     """(address, stride between rows) of a [rows, D] tensor whose rows are contiguous."""
     if t is None:
         return None, 0
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on GPU {dev}, got {t.device}")
-    if t.shape != (rows, D):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, D)}")
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.get_device() == dev and t.shape == (rows, D)):
+        _refuse(dev, t, name, dtypes, (rows, D))
     s = t.stride()
     if D > 1 and s[1] != 1:
         raise ValueError(f"{name}: each row must be contiguous, got strides {s}")
