@@ -866,12 +866,6 @@ int kda_block_norm(const void *resid, int64_t resid_stride, const uint16_t *z, i
   if (!aligned(resid, rb) || !aligned(resid_out, rb) || !aligned(y, yb) || !aligned(z, 2) || !aligned(gate, 2) ||
       !aligned(w_post, 4) || !aligned(w_pre, 4))
     return KDA_ERR_ALIGN;
-  const auto row16 = [](const void *p, int64_t stride, int bytes) {
-    return !p || (aligned(p, 16) && stride * bytes % 16 == 0);
-  };
-  const bool vec = D % 8 == 0 && row16(resid, resid_stride, rb) && row16(resid_out, resid_out_stride, rb) &&
-                   row16(z, z_stride, 2) && row16(gate, gate_stride, 2) && row16(y, y_stride, yb) &&
-                   row16(w_post, 0, 4) && row16(w_pre, 0, 4);
   NormArgs a;
   memset(&a, 0, sizeof a);
   a.resid = resid;
@@ -892,10 +886,9 @@ int kda_block_norm(const void *resid, int64_t resid_stride, const uint16_t *z, i
   a.D = D;
   a.resid_bf16 = rb == 2;
   a.y_bf16 = yb == 2;
-  int threads = 0;
-  const void *fn = norm_kernel_for(D, vec, &threads);
+  const NormLaunch l = norm_launch(rows, D, rb == 2);
   void *args[] = {&a};
-  const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)rows), dim3(threads), args, 0, (hipStream_t)stream);
+  const hipError_t e = hipLaunchKernel(l.fn, dim3((unsigned)l.blocks), dim3(l.threads), args, 0, (hipStream_t)stream);
   return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 

@@ -54,8 +54,11 @@ struct NormArgs {
   int32_t rows, D, resid_bf16, y_bf16;
 };
 
-// Launch shape and kernel of a block norm of width D (vec: every row is 16-byte
-// aligned and D is a multiple of 8).
-const void *norm_kernel_for(int D, bool vec, int *threads);
+// Kernel, threads and workgroups of a block norm.
+struct NormLaunch {
+  const void *fn;
+  int threads, blocks;
+};
+NormLaunch norm_launch(int rows, int D, bool resid_bf16);
 
 }  // namespace kda

@@ -40,9 +40,8 @@ enum kda_norm_flag { KDA_NORM_RESID_BF16 = 1, KDA_NORM_Y_BF16 = 2 };
  *   gate       bf16, or NULL
  *   w_pre      float [D]
  * At least one of z and y is needed. No other output may overlap an input or an
- * output. Pointers need their element's alignment only (KDA_ERR_ALIGN); rows
- * that are 16-byte aligned throughout, with D a multiple of 8, are read and
- * written 128 bits at a time. res_scale must be finite, eps finite and >= 0
+ * output. Pointers need their element's alignment only (KDA_ERR_ALIGN), and so
+ * do strides and D. res_scale must be finite, eps finite and >= 0
  * (KDA_ERR_INVALID); D in [1, KDA_NORM_MAX_D] (KDA_ERR_UNSUPPORTED past it).
  * rows == 0 enqueues nothing. Nothing is allocated; the kernel goes on `stream`.
  */
