@@ -1,4 +1,5 @@
-"""Build the HIP library for gfx950: gated_delta_rule_98_amd/libkda.so, and the
+"""Build the HIP library for gfx950: gated_delta_rule_98_amd/libkda.so, the native
+marshalling module beside it (kda_native.so, csrc/kda_binding.cpp) and the
 benchmark's HBM ceiling probes, gated_delta_rule_98_amd/libkda_ceiling.so.
 
 Sources (csrc/): kda_engine.h holds the device building blocks every kernel
@@ -31,6 +32,9 @@ LIB = os.path.join(PKG, "libkda.so")
 # the benchmark's ceiling probes (csrc/probe/): not part of the KDA library or its C ABI
 CEILING_SOURCES = [os.path.join(CSRC, "probe", "kda_ceiling.hip")]
 CEILING_LIB = os.path.join(PKG, "libkda_ceiling.so")
+# the argument marshalling of the linear-attention and norm calls (host code)
+NATIVE_SOURCE = os.path.join(CSRC, "kda_binding.cpp")
+NATIVE = os.path.join(PKG, "kda_native.so")
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -52,6 +56,26 @@ def build(out: str = LIB, extra=(), verbose: bool = False, sources=None) -> str:
         raise RuntimeError(f"hipcc failed ({r.returncode}):\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     if verbose and (r.stdout or r.stderr):
         print(r.stdout, r.stderr)
+    os.replace(tmp, out)
+    if out == LIB:  # the package needs both
+        build_native()
+    return out
+
+
+def build_native(out: str = NATIVE) -> str:
+    """Compile the native marshalling module (host code only; always recompiles); return its path."""
+    import sysconfig
+
+    from torch.utils import cpp_extension
+
+    tmp = f"{out}.tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-I{INCLUDE}",
+           f"-I{sysconfig.get_paths()['include']}", *(f"-isystem{p}" for p in cpp_extension.include_paths()),
+           NATIVE_SOURCE, "-o", tmp, *(f"-L{p}" for p in cpp_extension.library_paths()),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed ({r.returncode}):\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, out)
     return out
 

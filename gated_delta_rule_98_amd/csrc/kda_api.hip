@@ -740,6 +740,7 @@ int kda_lin_decode_step(float *cache, int64_t num_slots, int64_t slot_stride, co
   if (tile_w == 2) return KDA_ERR_UNSUPPORTED;
   KDA_TRY(choose_width(KIND_DECODE, B, H, dk, dv, epi != nullptr, tile_w, &l));
   if (l.C == 0) KDA_TRY(choose_width(KIND_DECODE, B, H, dk, dv, false, 4, &l));
+  if (epi) l = {dv, dv / (4 * kLinGateSlabs), kLinGateSlabs};
 
   a.cache = cache;
   a.num_slots = num_slots;

@@ -35,7 +35,7 @@ __device__ __forceinline__ void lin_token(float4 (&s)[C][NV], const float4 (&k)[
 
 // Single-token step, in place: one workgroup per (row, head, W value columns).
 template <int DK, int C, bool GATE, bool BF16>
-__global__ __launch_bounds__(GATE ? 1024 : 256) void lin_decode_kernel(LinArgs a) {
+__global__ __launch_bounds__(256) void lin_decode_kernel(LinArgs a) {
   constexpr int NV = DK / 64;
   const Unit u = unit_of_block(a.ntile, a.H);
   const Lane L = lane_geometry();
@@ -770,7 +770,7 @@ const void *lin_decode_io(bool bf16) {
 
 template <int DK>
 const void *lin_decode_for(int C, bool gate, bool bf16) {
-  if (gate) return C == kGateSlabsDecode ? lin_decode_io<DK, kGateSlabsDecode, true>(bf16) : nullptr;
+  if (gate) return C == kLinGateSlabs ? lin_decode_io<DK, kLinGateSlabs, true>(bf16) : nullptr;
   switch (C) {
     case 1: return lin_decode_io<DK, 1, false>(bf16);
     case 2: return lin_decode_io<DK, 2, false>(bf16);

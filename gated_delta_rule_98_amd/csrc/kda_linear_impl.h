@@ -28,6 +28,11 @@ struct LinArgs {
   float *wdec;  // decays over a segment, [2 (units - B)][H]
 };
 
+// Slabs of columns per lane of the gated single-token step, whose workgroup owns
+// all dv columns of a head (waves = dv / (4 * slabs)). Measured on MI355X at 2, 4
+// and 8 slabs: 13 rows x 24 heads at 64 x 128 8.3, 7.7, 7.2 us; 8 x 32 at
+// 128 x 128 9.5, 8.8, 8.5; 64 x 32 46.8, 49.3, 47.7.
+constexpr int kLinGateSlabs = 8;
 const void *lin_decode_kernel_for(int dk, int C, bool gate, bool bf16);
 
 constexpr int kLinChunk = 64;    // tokens per chunk of the prefill
