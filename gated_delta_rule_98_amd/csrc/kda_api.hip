@@ -760,21 +760,39 @@ int kda_lin_decode_step(float *cache, int64_t num_slots, int64_t slot_stride, co
                     a, stream);
 }
 
-// Chunks per segment of a prefill and the segments past the rows' first ones.
-// A segment is long enough that about 512 (unit, head) workgroups share the
-// chunks, two per CU, and at least 4 chunks. Rows that hold at most that many
-// are one segment. A row of n tokens has at most (n - 1) / 64 chunks after its
-// first, so the rows together have at most n_tok / 64 / seg segments after
-// their first ones.
+// Prefill takes one workgroup per (row, head, 16 value columns) that walks the
+// row (lin_walk_kernel) for short prompts of few heads, else one per (segment,
+// head). Measured on MI355X, us, walking / in segments: one row of 32 heads,
+// 128 x 128: 37 tokens 6.8 / 11.3, 256 tokens 14.4 / 26, 512 24.6 / 31, 768
+// 34.4 / 34, 1024 43.5 / 38; 64 x 64: 512 tokens 15.5 / 19, 1024 28.7 / 23.5.
+// 512 workgroups: 8 rows x 8 heads of 512 tokens 19.0 / 26.6, 2 x 32 of 256
+// 17.8 / 17.0; 1024 workgroups: 4 x 32 of 256 23.7 / 12.8.
+static bool lin_walks(int32_t B, int32_t n_tok, int32_t H, int32_t dv) {
+  return (int64_t)B * H * lin_walk_tiles(dv) <= 512 && n_tok <= 640;
+}
+
+// Chunks per segment and the segments past the rows' first ones. Many chunks are
+// shared by about 512 (segment, head) workgroups, two per CU: cutting further
+// moves more states, cutting less leaves CUs idle (8000 tokens x 32 heads, us, at
+// 256, 512 and 1024 workgroups: 167, 153, 168). Few are cut to about 256, but to
+// no less than 2 and no more than 4 chunks each, where a chunk's latency counts
+// against that of chaining the segments (1024 tokens x 32 heads, 2 and 4 chunks:
+// 38, 44; 2048 x 32: 60, 53; 2048 x 8: 33, 42; 8000 x 8: 70, 60); with rows of
+// under 4 chunks on average not below 4, since rows that need no cut would still
+// pay for three launches (4 rows of 64 tokens x 32 heads: 18, 12.8). Rows of at
+// most that many chunks are one segment. A row of n tokens has at most
+// (n - 1) / 64 chunks after its first, so the rows together have at most
+// (n_tok - 1) / 64 / seg segments after their first ones.
 struct LinSplit {
   int32_t seg;
   int64_t more;
 };
 
 static LinSplit lin_split(int32_t B, int32_t n_tok, int32_t H) {
-  const int64_t chunks = (int64_t)n_tok / kLinChunk + B;
-  const int64_t seg = std::min<int64_t>(std::max<int64_t>(4, (chunks * H + 511) / 512), 1 << 24);
-  return {(int32_t)seg, n_tok / kLinChunk / seg};
+  const int64_t chunks = n_tok / kLinChunk;
+  const int64_t few = chunks < 4 * (int64_t)B ? 4 : std::min<int64_t>(4, std::max<int64_t>(2, (chunks * H + 255) / 256));
+  const int64_t seg = std::min<int64_t>(std::max<int64_t>(few, ((chunks + B) * H + 511) / 512), 1 << 24);
+  return {(int32_t)seg, n_tok > 0 ? (n_tok - 1) / kLinChunk / seg : 0};
 }
 
 static size_t lin_ws_state_bytes(const LinSplit &s, int32_t H, int32_t dk, int32_t dv) {
@@ -784,7 +802,7 @@ static size_t lin_ws_state_bytes(const LinSplit &s, int32_t H, int32_t dk, int32
 int kda_lin_prefill_workspace(int32_t B, int32_t n_tok, int32_t H, int32_t dk, int32_t dv, size_t *bytes) {
   if (!bytes || B < 0 || n_tok < 0 || H <= 0 || dk <= 0 || dv <= 0) return KDA_ERR_INVALID;
   if (!dims_supported(dk, dv)) return KDA_ERR_UNSUPPORTED;
-  const LinSplit s = lin_split(B, n_tok, H);
+  const LinSplit s = lin_walks(B, n_tok, H, dv) ? LinSplit{0, 0} : lin_split(B, n_tok, H);
   // a state for every segment of a row that has two or more, then their decays
   *bytes = lin_ws_state_bytes(s, H, dk, dv) + ((size_t)(2 * s.more) * H * sizeof(float) + 15) / 16 * 16;
   return KDA_OK;
@@ -831,6 +849,12 @@ int kda_lin_prefill(float *cache, int64_t num_slots, int64_t slot_stride, const 
   a.H = H;
   a.dv = dv;
   a.n_tok = n_tok;
+  if (lin_walks(B, n_tok, H, dv)) {
+    if (n_tok == 0) a.group = 1;  // no tokens, no key heads
+    const int64_t groups = ((int64_t)B * (H / a.group) + 7) / 8 * 8;  // dealt to the 8 XCDs
+    return launch_lin(lin_walk_kernel_for(dk, a.out_bf16), groups * a.group * lin_walk_tiles(dv), lin_walk_threads(dk), a,
+                      stream);
+  }
   const LinSplit s = lin_split(B, n_tok, H);
   a.seg = s.seg;
   const int64_t units = B + s.more;

@@ -198,6 +198,18 @@ __device__ __forceinline__ bf16x8 ld_tokens(const uint16_t *base, int tok0, int 
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// The same at tokens 4 g .. + 3 and 16 + 4 g .. + 3, where two accumulator tiles
+// whose rows are tokens have theirs.
+template <int PITCH>
+__device__ __forceinline__ bf16x8 ld_tokens2(const uint16_t *base, int tok0, int col0) {
+  typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
+  const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
+  const uint16_t *p = base + (tok0 + 4 * g + (i >> 2)) * PITCH + col0 + 4 * (i & 3);
+  const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)p);
+  const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 16 * PITCH));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
 // 8 channels of one token: contiguous, or the two runs of 4 at which the lane's
 // accumulator registers of two 16-channel tiles stand.
 __device__ __forceinline__ bf16x8 ld_run8(const uint16_t *p) {
@@ -761,6 +773,299 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
   if (seg + 1 == r.nseg) S.store(slot, false);
 }
 
+// ----------------------------------------------------------------------------
+// Short prompts of few heads: a workgroup per 16 value columns
+// ----------------------------------------------------------------------------
+//
+// With few (row, head) pairs the kernel above leaves most CUs idle and a chunk
+// takes it 5 us. Here a workgroup has 16 columns of a head and walks the whole
+// row, its waves in two roles, one barrier per chunk. DK / 32 waves carry the
+// state: S0^T q_t over the wave's 32 channels, to LDS, then the update. Six waves
+// take the scores' products with v, up to 2 score tiles each, split in registers
+// in the layout in which the product takes them: 16 tokens against 32 earlier
+// ones. One chunk later four of them add up their tokens' terms and write.
+// A chunk is requested two chunks ahead (two register sets rotate) and written to
+// LDS one ahead. Every column tile forms the scores again, so this costs more
+// work in total than the kernel above; lin_walks (kda_api.hip) says where it wins.
+
+constexpr int kWalkTile = 16, kWalkOutWaves = 6;
+
+// Token-major arrays of one chunk.
+template <int DK>
+struct WalkTokens {
+  static constexpr int PITCH = DK + 8;  // padded against bank conflicts
+  uint16_t q[kLinChunk * PITCH], k[kLinChunk * PITCH], v[kLinChunk * kWalkTile];
+};
+
+// A chunk's q, k and v tile on their way from memory to LDS, in 16-byte pieces
+// spread over NW waves: pieces of 64 lanes, those of k, then those of q, and two
+// of v. Tokens past the chunk's nt as in Staged16.
+template <int DK, int NW>
+struct WalkLoad {
+  static constexpr int CP = DK / 8;     // 16-byte pieces of a token = pieces of 64 lanes of an array
+  static constexpr int ROWS = 64 / CP;  // tokens per piece of 64 lanes
+  static constexpr int WP = 2 * CP, N = (WP + NW - 1) / NW;
+  u32x4 x[N], xv;
+
+  __device__ static const u32x4 *at(const uint16_t *base, uint32_t bytes) {
+    return reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(base) + bytes);
+  }
+  __device__ __forceinline__ void load(const LinArgs &a, const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                                       int wave, int t0, int nt) {
+    const int lane = threadIdx.x & 63, r = lane / CP, c = (lane % CP) * 16;
+#pragma unroll
+    for (int m = 0; m < N; ++m) {
+      const int wp = wave + NW * m;
+      if (WP % NW == 0 || wp < WP) {
+        const bool isq = wp >= CP;
+        const int row0 = (isq ? wp - CP : wp) * ROWS;
+        const int64_t st = isq ? a.qs : a.ks;
+        const uint16_t *base = (isq ? q : k) + (int64_t)t0 * st;
+        if (nt == kLinChunk)
+          x[m] = *at(base + row0 * st, pinned(r * (uint32_t)(2 * st) + c));
+        else
+          x[m] = *at(base, pinned(min(row0 + r, nt - 1) * (uint32_t)(2 * st) + c));
+      }
+    }
+    if (wave < 2)
+      xv = *at(v + (int64_t)t0 * a.vs, pinned(min(32 * wave + (lane >> 1), nt - 1) * (uint32_t)(2 * a.vs) + (lane & 1) * 16));
+  }
+  __device__ __forceinline__ void store(WalkTokens<DK> &to, int wave, int nt) {
+    constexpr int PITCH = WalkTokens<DK>::PITCH;
+    const int lane = threadIdx.x & 63, r = lane / CP, c = (lane % CP) * 8;
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int m = 0; m < N; ++m) {
+      const int wp = wave + NW * m;
+      if (WP % NW == 0 || wp < WP) {
+        const bool isq = wp >= CP;
+        const int row = (isq ? wp - CP : wp) * ROWS + r;
+        if (nt < kLinChunk && row >= nt) x[m] = zero;
+        *reinterpret_cast<u32x4 *>((isq ? to.q : to.k) + row * PITCH + c) = x[m];
+      }
+    }
+    if (wave < 2) {
+      const int row = 32 * wave + (lane >> 1);
+      if (nt < kLinChunk && row >= nt) xv = zero;
+      *reinterpret_cast<u32x4 *>(to.v + row * kWalkTile + (lane & 1) * 8) = xv;
+    }
+  }
+};
+
+// The part of a state that one wave holds: 32 key channels x 16 columns, the
+// accumulator layout of two MFMA tiles: channels 16 i + 4 g .. + 3 of column m.
+struct WaveState {
+  v4f s[2];
+
+  // address of the wave's part of a [dv][dk] state, for this lane
+  __device__ static int64_t at(int dk, int tile, int r) {
+    const int lane = threadIdx.x & 63;
+    return (int64_t)(kWalkTile * tile + (lane & 15)) * dk + 32 * r + 4 * (lane >> 4);
+  }
+  __device__ __forceinline__ void load(const float *p) {
+    s[0] = *reinterpret_cast<const v4f *>(p);
+    s[1] = *reinterpret_cast<const v4f *>(p + 16);
+  }
+  __device__ __forceinline__ void store(float *p) const {
+    *reinterpret_cast<v4f *>(p) = s[0];
+    *reinterpret_cast<v4f *>(p + 16) = s[1];
+  }
+  __device__ __forceinline__ void zero() { s[0] = s[1] = (v4f){0.0f, 0.0f, 0.0f, 0.0f}; }
+
+  // S <- Gamma_L S + sum_s end_s k_s v_s^T over channels 32 r .. + 31
+  template <int DK>
+  __device__ __forceinline__ void update(const WalkTokens<DK> &x, const ChunkDecay &d, int r) {
+    const int g = (threadIdx.x & 63) >> 4;
+    bf16x8 kt[2][2];
+    Split3 vs[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) kt[kb][i] = ld_tokens<DK + 8>(x.k, 32 * kb, 32 * r + 16 * i);
+      const bf16x8 v = ld_tokens<kWalkTile>(x.v, 32 * kb, 0);
+      const float4 f0 = *reinterpret_cast<const float4 *>(d.end + 32 * kb + 8 * g);
+      const float4 f1 = *reinterpret_cast<const float4 *>(d.end + 32 * kb + 8 * g + 4);
+      const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+      vs[kb] = scaled_values(v, f);
+    }
+    const float gl = d.gam[kLinChunk - 1];
+    s[0] *= gl;
+    s[1] *= gl;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      s[0] = mma(kt[kb][0], vs[kb].lo, s[0]);
+      s[1] = mma(kt[kb][1], vs[kb].lo, s[1]);
+    }
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      s[0] = mma(kt[kb][0], vs[kb].mid, s[0]);
+      s[1] = mma(kt[kb][1], vs[kb].mid, s[1]);
+    }
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      s[0] = mma(kt[kb][0], vs[kb].hi, s[0]);
+      s[1] = mma(kt[kb][1], vs[kb].hi, s[1]);
+    }
+  }
+};
+
+template <int DK, bool BF16>
+__global__ __launch_bounds__(lin_walk_threads(DK)) void lin_walk_kernel(LinArgs a) {
+  constexpr int NR = DK / 32, NW = NR + kWalkOutWaves, PITCH = DK + 8, T = kLinChunk / kLB;
+  __shared__ __align__(16) WalkTokens<DK> tok[2];
+  __shared__ __align__(16) ChunkDecay dec[2];
+  __shared__ v4f part[2][NR][T][64];  // state terms by (chunk parity, wave, 16 tokens)
+  __shared__ v4f early[2][2][64];     // products with the first 32 tokens, of tokens 48.. and 32..
+  // the column tiles of a head, and the heads of a key head, are one XCD's in a row
+  const int hk = a.H / a.group;
+  int j, tile, in_group, row, kh;
+  divmod_uniform(blockIdx.x >> 3, a.dv / kWalkTile, j, tile);
+  divmod_uniform(j, a.group, j, in_group);
+  divmod_uniform(8 * j + (blockIdx.x & 7), hk, row, kh);
+  if (row >= a.B) return;
+  const int h = kh * a.group + in_group;
+  int32_t slot_id, c0;
+  int n;
+  const int err = lin_row_check(a, row, slot_id, c0, n);
+  if (err) {
+    if (err > 0 && h == 0 && tile == 0 && threadIdx.x == 0 && a.dev_err) atomicOr(a.dev_err, err);
+    return;
+  }
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+  const int ck = a.ckpt_pos ? a.ckpt_pos[row] : -1;
+  if (n == 0 && ck != 0) return;
+  const LinChunks chunks(n, ck);
+  const int64_t tok0 = c0;
+  const uint16_t *q = a.q + tok0 * a.qs + (int64_t)(h / a.group) * DK;
+  const uint16_t *k = a.k + tok0 * a.ks + (int64_t)(h / a.group) * DK;
+  const uint16_t *v = a.v + tok0 * a.vs + (int64_t)h * a.dv + kWalkTile * tile;
+  const float *al = a.alpha + tok0 * a.as + h;
+
+  WalkLoad<DK, NW> x[2];
+  float an[2] = {1.0f, 1.0f};
+  const auto load = [&](int c, int p) {
+    int t0, nt;
+    chunks.at(c, t0, nt);
+    if (nt == 0) return;
+    if (wave == NW - 1) an[p] = lane < nt ? al[(int64_t)(t0 + lane) * a.as] : 1.0f;
+    x[p].load(a, q, k, v, wave, t0, nt);
+  };
+  const auto put = [&](int c, int p) {
+    int t0, nt;
+    chunks.at(c, t0, nt);
+    if (nt == 0) return;
+    x[p].store(tok[p], wave, nt);
+    if (wave == NW - 1) put_chunk_decay(dec[p], an[p]);
+  };
+  if (n > 0) {
+    load(0, 0);
+    load(1, 1);
+    put(0, 0);
+  }
+
+  if (wave < NR) {
+    float *slot = a.cache + (int64_t)slot_id * a.slot_stride + (int64_t)h * (DK * a.dv) + WaveState::at(DK, tile, wave);
+    float *ckpt = ck >= 0 ? a.ckpt + ((int64_t)row * a.H + h) * (DK * a.dv) + WaveState::at(DK, tile, wave) : nullptr;
+    WaveState S;
+    S.load(slot);
+    if (ck == 0) S.store(ckpt);
+    if (n == 0) return;
+    __syncthreads();
+    const auto step = [&](int c, int p) {
+      load(c + 2, p);
+      const float xs[8] = {S.s[0][0], S.s[0][1], S.s[0][2], S.s[0][3], S.s[1][0], S.s[1][1], S.s[1][2], S.s[1][3]};
+      const Split3 sp = split3(xs);
+      bf16x8 qv[T];
+#pragma unroll
+      for (int tt = 0; tt < T; ++tt) qv[tt] = ld_run4x2(tok[p].q + (kLB * tt + m) * PITCH + 32 * wave + 4 * g);
+      v4f o[T];
+#pragma unroll
+      for (int tt = 0; tt < T; ++tt) o[tt] = mma(sp.lo, qv[tt], (v4f){0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+      for (int tt = 0; tt < T; ++tt) o[tt] = mma(sp.mid, qv[tt], o[tt]);
+#pragma unroll
+      for (int tt = 0; tt < T; ++tt) o[tt] = mma(sp.hi, qv[tt], o[tt]);
+#pragma unroll
+      for (int tt = 0; tt < T; ++tt) part[p][wave][tt][lane] = o[tt];
+      S.update<DK>(tok[p], dec[p], wave);
+      int t0, nt;
+      chunks.at(c, t0, nt);
+      if (t0 + nt == ck) S.store(ckpt);
+      put(c + 1, p ^ 1);
+      __syncthreads();
+    };
+    for (int c = 0; c < chunks.count; c += 2) {
+      step(c, 0);
+      if (c + 1 < chunks.count) step(c + 1, 1);
+    }
+    S.store(slot);
+    return;
+  }
+
+  if (n == 0) return;
+  __syncthreads();
+  // this wave's tokens 16 tt .. + 15 against 32 kb .. + 31; the waves of kb = tt / 2 write
+  const int f = wave - NR, tt = f < 4 ? 3 - f / 2 : 5 - f, kb = f == 0 || f == 2 ? 1 : 0;
+  const bool writes = kb == tt / 2;
+  v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  float gam = 0.0f;
+  constexpr int OB = BF16 ? 2 : 4;  // bytes of an output
+  const int64_t orow = (int64_t)a.H * a.dv;
+  const auto finish = [&](int c, int p) {
+    v4f o = part[p][0][tt][lane];
+#pragma unroll
+    for (int w = 1; w < NR; ++w) o += part[p][w][tt][lane];
+    o = o * gam + acc;
+    if (tt >= 2) o += early[p][3 - tt][lane];
+    int t0, nt;
+    chunks.at(c, t0, nt);
+    if (kLB * tt + m < nt) {
+      char *to = static_cast<char *>(a.out) + OB * ((tok0 + t0 + kLB * tt) * orow + (int64_t)h * a.dv + kWalkTile * tile) +
+                 pinned(OB * (m * (uint32_t)orow + 4 * g));
+      if constexpr (BF16) {
+        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+        *reinterpret_cast<bf16x4 *>(to) = __builtin_convertvector(o, bf16x4);
+      } else {
+        *reinterpret_cast<v4f *>(to) = o;
+      }
+    }
+  };
+  const auto step = [&](int c, int p) {
+    load(c + 2, p);
+    if (c > 0 && writes) finish(c - 1, p ^ 1);
+    bf16x8 qv[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) qv[i] = ld_run8(tok[p].q + (kLB * tt + m) * PITCH + 32 * i + 8 * g);
+    gam = dec[p].gam[kLB * tt + m];
+    float ps[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int st = 2 * kb + i;
+      float D[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      v4f sc = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (st <= tt) {
+#pragma unroll
+        for (int e = 0; e < NR; ++e)
+          sc = mma(ld_run8(tok[p].k + (kLB * st + m) * PITCH + 32 * e + 8 * g), qv[e], sc);
+        tile_decay(dec[p], st, tt, D);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ps[4 * i + e] = st < tt || (st == tt && m >= 4 * g + e) ? sc[e] * D[e] : 0.0f;
+    }
+    const Split3 sp = split3(ps);
+    const bf16x8 vv = ld_tokens2<kWalkTile>(tok[p].v, 32 * kb, 0);
+    acc = mma(vv, sp.hi, mma(vv, sp.mid, mma(vv, sp.lo, (v4f){0.0f, 0.0f, 0.0f, 0.0f})));
+    if (!writes) early[p][3 - tt][lane] = acc;
+    put(c + 1, p ^ 1);
+    __syncthreads();
+  };
+  for (int c = 0; c < chunks.count; c += 2) {
+    step(c, 0);
+    if (c + 1 < chunks.count) step(c + 1, 1);
+  }
+  if (writes) finish(chunks.count - 1, (chunks.count - 1) & 1);
+}
+
 }  // namespace
 
 template <int DK, int C, bool GATE>
@@ -790,6 +1095,10 @@ const void *lin_decode_kernel_for(int dk, int C, bool gate, bool bf16) {
 
 const void *lin_sum_kernel_for(int dk, int dv) { return KDA_LIN_DIMS(lin_sum_kernel); }
 const void *lin_scan_kernel_for(int dk, int dv) { return KDA_LIN_DIMS(lin_scan_kernel); }
+const void *lin_walk_kernel_for(int dk, bool bf16) {
+  if (dk == 64) return bf16 ? (const void *)lin_walk_kernel<64, true> : (const void *)lin_walk_kernel<64, false>;
+  return bf16 ? (const void *)lin_walk_kernel<128, true> : (const void *)lin_walk_kernel<128, false>;
+}
 const void *lin_out_kernel_for(int dk, int dv, bool bf16) {
   return bf16 ? KDA_LIN_DIMS(lin_out_kernel, , true) : KDA_LIN_DIMS(lin_out_kernel, , false);
 }

@@ -45,6 +45,10 @@ inline constexpr int lin_threads(int dv) { return 4 * dv; }
 const void *lin_sum_kernel_for(int dk, int dv);
 const void *lin_scan_kernel_for(int dk, int dv);
 const void *lin_out_kernel_for(int dk, int dv, bool bf16);
+// The kernel for short prompts of few heads: workgroups per (row, head) and threads.
+const void *lin_walk_kernel_for(int dk, bool bf16);
+inline constexpr int lin_walk_tiles(int dv) { return dv / 16; }
+inline constexpr int lin_walk_threads(int dk) { return 2 * dk + 6 * 64; }
 // Workgroups of the scan per (row, head).
 inline constexpr int lin_scan_parts(int dk, int dv) { return dk * dv / 4 / lin_threads(dv); }
 

@@ -196,7 +196,10 @@ LENS = [[1], [0, 1, 2, 3], [15, 16, 17], [31, 32, 33], [63, 64, 65], [127, 0, 12
 
 @pytest.mark.parametrize("lens", LENS, ids=str)
 @pytest.mark.parametrize("H,Hk,dk,dv,per_token,bf16", [
-    (2, 2, 128, 128, True, False), (6, 2, 64, 128, False, True), (3, 1, 128, 64, True, True), (4, 4, 64, 64, False, False)])
+    (2, 2, 128, 128, True, False), (6, 2, 64, 128, False, True), (3, 1, 128, 64, True, True), (4, 4, 64, 64, False, False),
+    # more than 512 (row, head, 16 columns): the kernel of whole heads
+    (72, 8, 128, 128, True, True), (80, 16, 64, 128, False, False), (136, 8, 128, 64, True, False),
+    (132, 132, 64, 64, True, True)])
 def test_prefill(lens, H, Hk, dk, dv, per_token, bf16):
     log(f"lin prefill lens={lens} H={H} Hk={Hk} dk={dk} dv={dv} per_token={per_token} bf16={bf16}")
     p = inputs(sum(lens) + H, sum(lens) + 3, H, Hk, dk, dv, per_token, fused=bf16)
@@ -208,27 +211,30 @@ def test_prefill(lens, H, Hk, dk, dv, per_token, bf16):
 
 
 @pytest.mark.parametrize("decay", ["zeros", "signed", "ones"])
-@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64)])
-def test_prefill_decays(decay, dk, dv):
+@pytest.mark.parametrize("dk,dv,H", [(128, 128, 8), (64, 64, 8), (128, 128, 24), (64, 64, 48)])
+def test_prefill_decays(decay, dk, dv, H):
     """Decays that forget the state outright, underflow inside a chunk, change sign, or keep everything."""
     lens = [130, 70, 16]
-    log(f"lin prefill decays={decay} dk={dk}")
-    p = inputs(17, sum(lens), 8, 4, dk, dv, True, decay=decay)
+    log(f"lin prefill decays={decay} dk={dk} H={H}")
+    p = inputs(17, sum(lens), H, 4, dk, dv, True, decay=decay)
     slots = slot_table(1, 3, 4)
-    cache0 = cache_of(2, 4, 8, dv, dk)
+    cache0 = cache_of(2, 4, H, dv, dk)
     got = run_prefill(p, lens, slots, cache0)
     check_prefill(p, lens, slots, cache0, got)
 
 
 @pytest.mark.parametrize("dk,dv", [(128, 128), (64, 128)])
-@pytest.mark.parametrize("H", [1, 4])
-def test_prefill_checkpoints(dk, dv, H):
+@pytest.mark.parametrize("H", [1, 4, 24])
+@pytest.mark.parametrize("long", [False, True])
+def test_prefill_checkpoints(dk, dv, H, long):
     """Checkpoints before, at and after chunk edges, at both ends of a row, in empty and padding rows."""
     lens = [70, 200, 64, 128, 1, 0, 0, 333, 40, 65, 129]
     pos = np.array([1, 63, 64, 65, 1, 0, -1, 256, 0, 65, 127], np.int32)
+    if not long:  # up to 640 tokens
+        lens, pos = lens[:6] + [0, 40, 65], np.array([1, 63, 64, 65, 1, 0, -1, 0, 65], np.int32)
     slots = slot_table(4, len(lens), len(lens) + 1)
-    slots[8] = -1
-    log(f"lin prefill checkpoints dk={dk} H={H}")
+    slots[lens.index(40)] = -1
+    log(f"lin prefill checkpoints dk={dk} H={H} {sum(lens)} tokens")
     p = inputs(23, sum(lens), H, H, dk, dv, True)
     cache0 = cache_of(2, len(lens) + 1, H, dv, dk)
     got = run_prefill(p, lens, slots, cache0, pos=pos)
@@ -260,10 +266,11 @@ def test_prefill_checkpoint_without_tokens():
     check_prefill(p, [0, 0, 0], np.array([1, 0, 2], np.int32), cache0, got, pos=pos)
 
 
-def test_prefill_row_errors_skip_the_row():
+@pytest.mark.parametrize("H", [3, 24])
+def test_prefill_row_errors_skip_the_row(H):
     """A slot past the cache, a decreasing range, one past n_tok, a checkpoint past the row: the bit is set,
     the row is skipped in full, the others are right."""
-    H, dk, dv = 3, 128, 128
+    dk, dv = 128, 128
     lens = [40, 50, 70]
     p = inputs(41, sum(lens), H, 1, dk, dv, True)
     cache0 = cache_of(2, 5, H, dv, dk)
@@ -307,10 +314,11 @@ def test_decode_row_errors():
     assert torch.equal(cache[1:].cpu(), cache0[1:])
 
 
-def test_nonfinite_inputs_stay_in_their_row_and_head():
+@pytest.mark.parametrize("H", [4, 24])
+def test_nonfinite_inputs_stay_in_their_row_and_head(H):
     """NaN and infinity in the tokens, decays and state of one row and head leave every other row and head the
     bits they have without them."""
-    lens, H, d = [70, 66, 150], 4, 128
+    lens, d = [70, 66, 150], 128
     p = inputs(51, sum(lens) + 1, H, H, d, d, True)
     cache0 = cache_of(2, 4, H, d, d)
     slots = np.array([3, 1, 0], np.int32)
@@ -334,16 +342,17 @@ def test_nonfinite_inputs_stay_in_their_row_and_head():
             assert np.array_equal(bits(got[1][slots[b], h]), bits(clean[1][slots[b], h])), (b, h)
 
 
-def test_prefill_matches_decode_steps():
-    """A prompt in one call, and the same tokens one call each."""
-    T, H, Hk, d = 150, 4, 2, 128
+@pytest.mark.parametrize("T,H,Hk", [(150, 4, 2), (150, 72, 8), (700, 2, 2)])
+def test_prefill_matches_decode_steps(T, H, Hk):
+    """A prompt in one call (each of the ways in which the library runs one), and the same tokens one call each."""
+    d = 128
     p = inputs(61, T, H, Hk, d, d, True)
     cache0 = cache_of(2, 2, H, d, d)
     one = run_prefill(p, [T], np.array([1], np.int32), cache0)
     q, k, v = (t.to(dev()) for t in split(p, p["x"]))
     cache, out, al = cache0.to(dev()), torch.empty(T, H, d, device=dev()), p["alpha"].to(dev())
     s = i32([1])
-    log("lin decode, 150 steps")
+    log(f"lin decode, {T} steps")
     for t in range(T):
         K.kda_lin_decode_step(cache, s, q[t: t + 1], k[t: t + 1], v[t: t + 1], al[t: t + 1], out[t: t + 1])
     torch.cuda.synchronize()
@@ -400,6 +409,48 @@ def test_workspace_given_by_the_caller():
         with pytest.raises(K.KdaError) as e:
             run_prefill(p, lens, slots, cache0, workspace=ws[: need - 1])
         assert e.value.status == K.KDA_ERR_INVALID
+
+
+def test_overlapping_rows_are_run_or_reported():
+    """A table whose rows overlap (each range valid by itself) asks for more segments than the library plans for:
+    every row either has its right state or is left alone and reported."""
+    n, H, d, B = 2000, 2, 64, 9
+    p = inputs(95, n, H, H, d, d, True)
+    cache0 = cache_of(2, B, H, d, d)
+    q, k, v = split(p, p["x"].to(dev()))
+    cu = [0, n] * 5  # even rows [0, n), odd rows decreasing
+    cache, out = cache0.to(dev()), torch.empty(n, H, d, device=dev())
+    err = torch.zeros(1, dtype=torch.int32, device=dev())
+    log("lin prefill with overlapping rows")
+    K.kda_lin_prefill(cache, i32(np.arange(B)), i32(cu), q, k, v, p["alpha"].to(dev()), out, dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == K.KDA_DEVERR_SEQLEN
+    ran = 0
+    for b in range(B):
+        if torch.equal(cache[b].cpu(), cache0[b]):
+            continue
+        assert b % 2 == 0
+        args = split(p, p["x"]) + (p["alpha"], cache0[b])
+        _, S, _ = R.recur(*args)
+        _, SA, _ = R.recur(*args, absolute=True)
+        R.check(cache[b], S, R.roundings(n, 0) * R.U32 * SA + 1e-37, f"state of row {b}")
+        ran += 1
+    assert ran >= 1
+
+
+def test_many_rows():
+    """More rows than a wave has lanes: the search for a workgroup's row goes on past the first 64."""
+    lens = [(7 * b) % 90 for b in range(150)]
+    lens[97] = 900
+    H, d = 2, 64
+    pos = np.array([n // 2 if b % 3 else -1 for b, n in enumerate(lens)], np.int32)
+    p = inputs(96, sum(lens), H, 1, d, d, True)
+    slots = slot_table(5, len(lens), len(lens))
+    cache0 = cache_of(2, len(lens), H, d, d)
+    log(f"lin prefill with {len(lens)} rows")
+    got = run_prefill(p, lens, slots, cache0, pos=pos)
+    assert got[3] == 0
+    check_prefill(p, lens, slots, cache0, got, pos=pos)
 
 
 def test_offsets_past_32_bits():
