@@ -50,7 +50,11 @@ def check(got, ref, bound, what):
 
 
 def out_bound(A, T, dk, ref, bf16):
-    return roundings(T, dk) * U32 * A + (UB16 * ref.abs() * (1 + 1e-3) if bf16 else 0) + 1e-37
+    """bf16 outputs may be formed from operands in two bf16 parts, hi = x rounded and lo = x - hi rounded: x - hi is
+    within 2^-9 of x (half a step of 8 bits), the rounding of lo within 2^-9 of that, so each term is off by at
+    most 2^-18 of itself (64 u) besides the fp32 roundings."""
+    c = roundings(T, dk) + (64 if bf16 else 0)
+    return c * U32 * A + (UB16 * ref.abs() * (1 + 1e-3) if bf16 else 0) + 1e-37
 
 
 def gated(o, gate, weight, eps):
