@@ -857,18 +857,18 @@ int kda_lin_prefill(float *cache, int64_t num_slots, int64_t slot_stride, const 
   }
   const LinSplit s = lin_split(B, n_tok, H);
   a.seg = s.seg;
-  const int64_t units = B + s.more;
-  if (units * H > 0x7ffffff0) return KDA_ERR_UNSUPPORTED;
-  a.units = (int32_t)units;
+  a.more = (int32_t)s.more;
   a.ws = static_cast<float *>(workspace);
   a.wdec = reinterpret_cast<float *>(static_cast<char *>(workspace) + lin_ws_state_bytes(s, H, dk, dv));
   if (n_tok == 0) a.group = 1;  // no tokens, no key heads
-  const int64_t blocks = (units * (H / a.group) + 7) / 8 * 8 * a.group;
+  // workgroups for (unit, head), the (unit, key head) pairs dealt to the 8 XCDs
+  const auto blocks = [&](int64_t units) { return (units * (H / a.group) + 7) / 8 * 8 * a.group; };
+  if (blocks(B + s.more) > 0x7fffffff) return KDA_ERR_UNSUPPORTED;
   if (s.more > 0) {
-    KDA_TRY(launch_lin(lin_sum_kernel_for(dk, dv), blocks, lin_threads(dv), a, stream));
+    KDA_TRY(launch_lin(lin_sum_kernel_for(dk, dv), blocks(s.more), lin_threads(dv), a, stream));
     KDA_TRY(launch_lin(lin_scan_kernel_for(dk, dv), (int64_t)B * H * lin_scan_parts(dk, dv), lin_threads(dv), a, stream));
   }
-  return launch_lin(lin_out_kernel_for(dk, dv, a.out_bf16), blocks, lin_threads(dv), a, stream);
+  return launch_lin(lin_out_kernel_for(dk, dv, a.out_bf16), blocks(B + s.more), lin_threads(dv), a, stream);
 }
 
 // ------------------------------------------------------------------ block norm

@@ -305,13 +305,12 @@ __device__ __forceinline__ void put_chunk_decay(ChunkDecay &d, float al) {
   d.end[lane] = (float)(after * post);
 }
 
-// One row's tokens and its place in the numbering of units: a row has
-// max(1, ceil(chunks / seg)) units (one segment each; a row to skip has one,
-// which reports it), and a state slot per segment if it has more than one.
-// Units 0 .. a.units - 1 are launched, which holds every row of a table whose
-// rows do not overlap; a row past them is skipped and reported as a bad range.
+// One row's tokens and segments. The segments but a row's last are full and
+// numbered over all rows (full0 stand before this row's), a.more of them at most
+// in a table whose rows do not overlap; a row past that is skipped and reported
+// as a bad range. A row of two or more segments has a state slot for each.
 struct LinRow {
-  int b, unit0, slot0, nseg, n;
+  int b, full0, slot0, nseg, n;
   int32_t c0, slot;
   int err;  // 0, a device error, or -1 for a padding row
 };
@@ -330,8 +329,7 @@ __device__ __forceinline__ int lin_row_check(const LinArgs &a, int b, int32_t &s
 }
 
 __device__ __forceinline__ int lin_segments(const LinArgs &a, int n) {
-  const int chunks = (n + kLinChunk - 1) / kLinChunk;
-  return chunks > a.seg ? (chunks + a.seg - 1) / a.seg : 1;
+  return n > 0 ? (n - 1) / kLinChunk / a.seg + 1 : 1;
 }
 
 // Inclusive prefix sum over the wave: inside 16-lane rows, then the last lane
@@ -349,49 +347,56 @@ __device__ __forceinline__ int wave_prefix_sum(int x) {
   return dpp_add<0x143, 0xC>(x);
 }
 
-// The row that holds a unit (by_unit) or the row of that number, found by each
-// wave over 64 rows at a time; false where there is none.
-__device__ __forceinline__ bool lin_find(const LinArgs &a, bool by_unit, int key, LinRow &r) {
-  if (a.units == a.B || a.B == 1) {  // no row is cut (unit = row) or there is only one: no search
-    r.b = a.B == 1 ? 0 : key;
-    r.unit0 = r.b;
-    r.slot0 = 0;
-    r.err = lin_row_check(a, r.b, r.slot, r.c0, r.n);
-    r.nseg = lin_segments(a, r.n);
-    return key < r.unit0 + r.nseg;
-  }
+// Row `key`, or the row that holds full segment `key`, by a search over 64 rows
+// at a time that every wave does for itself; false where there is none.
+__device__ __forceinline__ bool lin_search(const LinArgs &a, bool full_segment, int key, LinRow &r) {
   const int lane = threadIdx.x & 63;
-  int units = 0, slots = 0;
+  int full = 0, slots = 0;
   for (int base = 0; base < a.B; base += 64) {
     const int b = base + lane;
     int32_t slot = -1, c0 = 0;
-    int n = 0, err = -1, nseg = 0;
+    int n = 0, err = -1, nseg = 1;
     if (b < a.B) {
       err = lin_row_check(a, b, slot, c0, n);
       nseg = lin_segments(a, n);
     }
-    const int iu = wave_prefix_sum(nseg);
-    const uint64_t hit = __ballot(b < a.B && (by_unit ? key < units + iu : b == key));
-    const uint64_t whole = __ballot(nseg == 1);  // rows without state slots
+    const int upto = wave_prefix_sum(nseg - 1);
+    const uint64_t hit = __ballot(b < a.B && (full_segment ? key < full + upto : b == key));
+    const uint64_t cut = __ballot(nseg > 1);
     if (hit) {
       const int l = __builtin_ctzll(hit);
       r.b = base + l;
       r.nseg = __builtin_amdgcn_readlane(nseg, l);
-      const int before = __builtin_amdgcn_readlane(iu, l) - r.nseg;
-      r.unit0 = units + before;
-      r.slot0 = slots + before - __builtin_popcountll(whole & ((1ull << l) - 1));
+      const int before = __builtin_amdgcn_readlane(upto, l) - (r.nseg - 1);
+      r.full0 = full + before;
+      r.slot0 = slots + before + __builtin_popcountll(cut & ((1ull << l) - 1));
       r.n = __builtin_amdgcn_readlane(n, l);
       r.c0 = __builtin_amdgcn_readlane(c0, l);
       r.slot = __builtin_amdgcn_readlane(slot, l);
       r.err = __builtin_amdgcn_readlane(err, l);
-      if (r.err == 0 && r.unit0 + r.nseg > a.units) r.err = KDA_DEVERR_SEQLEN;
+      if (r.err == 0 && r.nseg > 1 && r.full0 + r.nseg - 1 > a.more) r.err = KDA_DEVERR_SEQLEN;
       return true;
     }
-    const int all = __builtin_amdgcn_readlane(iu, 63);
-    units += all;
-    slots += all - __builtin_popcountll(whole);
+    const int all = __builtin_amdgcn_readlane(upto, 63);
+    full += all;
+    slots += all + __builtin_popcountll(cut);
   }
   return false;
+}
+
+__device__ __forceinline__ void lin_row(const LinArgs &a, int b, LinRow &r) {
+  r.b = b;
+  r.full0 = r.slot0 = 0;
+  r.err = lin_row_check(a, b, r.slot, r.c0, r.n);
+  r.nseg = lin_segments(a, r.n);
+  // where it stands matters only to a row that is cut
+  if (r.nseg > 1 && a.B > 1) lin_search(a, false, b, r);
+}
+
+__device__ __forceinline__ bool lin_full_segment(const LinArgs &a, int e, LinRow &r) {
+  if (a.B > 1) return lin_search(a, true, e, r);
+  lin_row(a, 0, r);
+  return e < r.nseg - 1;
 }
 
 // Workgroups are dispatched round-robin over the 8 XCDs. The (unit, key head)
@@ -399,13 +404,13 @@ __device__ __forceinline__ bool lin_find(const LinArgs &a, bool by_unit, int key
 // each other in one XCD's order, so that they read its q and k through one L2.
 // (Dealing whole units instead, so that a token's neighbouring heads meet in one
 // L2, measured the same on one long row and 15% slower on ragged ones.)
-__device__ __forceinline__ bool lin_unit_head(const LinArgs &a, int &unit, int &h) {
+__device__ __forceinline__ bool lin_unit_head(const LinArgs &a, int units, int &unit, int &h) {
   const int n = blockIdx.x, hk = a.H / a.group;
   int j, in_group, kh;
   divmod_uniform(n >> 3, a.group, j, in_group);
   divmod_uniform(8 * j + (n & 7), hk, unit, kh);
   h = kh * a.group + in_group;
-  return unit < a.units;
+  return unit < units;
 }
 
 // Accumulator layout of a state. Wave w holds value columns 16 w .. + 15; its
@@ -564,9 +569,8 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_sum_kernel(L
   __shared__ __align__(16) ChunkDecay dec[NW];
   int unit, h;
   LinRow r;
-  if (!lin_unit_head(a, unit, h) || !lin_find(a, true, unit, r) || r.err) return;
-  const int seg = unit - r.unit0;
-  if (seg + 1 >= r.nseg) return;
+  if (!lin_unit_head(a, a.more, unit, h) || !lin_full_segment(a, unit, r) || r.err) return;
+  const int seg = unit - r.full0;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t tok0 = (int64_t)r.c0 + (int64_t)seg * a.seg * kLinChunk;
   const uint16_t *k = a.k + tok0 * a.ks + (int64_t)(h / a.group) * DK;
@@ -622,7 +626,8 @@ __global__ __launch_bounds__(lin_threads(DV)) void lin_scan_kernel(LinArgs a) {
   divmod_uniform(blockIdx.x, lin_scan_parts(DK, DV), bh, ni);
   divmod_uniform(bh, a.H, b, h);
   LinRow r;
-  if (!lin_find(a, false, b, r) || r.err || r.nseg < 2) return;
+  lin_row(a, b, r);
+  if (r.err || r.nseg < 2) return;
   v4f s = *reinterpret_cast<const v4f *>(a.cache + (int64_t)r.slot * a.slot_stride + (int64_t)h * (DK * DV) +
                                          LinState<DK, DV>::at(ni));
   float *w = a.ws + ((int64_t)r.slot0 * a.H + h) * (DK * DV) + LinState<DK, DV>::ws_at(ni);
@@ -649,16 +654,20 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
   __shared__ __align__(16) ChunkDecay dec[NW];  // of a group of NW chunks
   int unit, h;
   LinRow r;
-  if (!lin_unit_head(a, unit, h)) return;
-  const bool found = lin_find(a, true, unit, r);
-  if (!found) return;
-  if (unit + 1 == a.units && r.b + 1 < a.B && r.unit0 + r.nseg <= a.units && h == 0 && threadIdx.x == 0 && a.dev_err)
-    atomicOr(a.dev_err, KDA_DEVERR_SEQLEN);  // rows past the launched units (only with rows that overlap)
-  if (r.err) {
-    if (r.err > 0 && unit == r.unit0 && h == 0 && threadIdx.x == 0 && a.dev_err) atomicOr(a.dev_err, r.err);
-    return;
+  // Full segments first, then every row's last one: the longest start first.
+  if (!lin_unit_head(a, a.more + a.B, unit, h)) return;
+  int seg;
+  if (unit < a.more) {
+    if (!lin_full_segment(a, unit, r) || r.err) return;  // reported with the row's last segment
+    seg = unit - r.full0;
+  } else {
+    lin_row(a, unit - a.more, r);
+    if (r.err) {
+      if (r.err > 0 && h == 0 && threadIdx.x == 0 && a.dev_err) atomicOr(a.dev_err, r.err);
+      return;
+    }
+    seg = r.nseg - 1;
   }
-  const int seg = unit - r.unit0;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
   const int ck = a.ckpt_pos ? a.ckpt_pos[r.b] : -1;
   float *slot = a.cache + (int64_t)r.slot * a.slot_stride + (int64_t)h * (DK * DV);

@@ -22,10 +22,10 @@ struct LinArgs {
   float eps;
   int32_t B, H, group, dv, n_tok, ntile;  // group = H / Hk heads share a key head
   int32_t out_bf16;
-  // prefill: segments of seg chunks; units = B + (segments past each row's first, at most)
-  int32_t seg, units;
-  float *ws;    // states, [2 (units - B)][H][dv dk]
-  float *wdec;  // decays over a segment, [2 (units - B)][H]
+  // prefill: segments of seg chunks; at most `more` segments that another of their row follows
+  int32_t seg, more;
+  float *ws;    // states, [2 more][H][dv dk]
+  float *wdec;  // decays over a segment, [2 more][H]
 };
 
 // Slabs of columns per lane of the gated single-token step, whose workgroup owns
