@@ -654,14 +654,16 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
   __shared__ __align__(16) ChunkDecay dec[NW];  // of a group of NW chunks
   int unit, h;
   LinRow r;
-  // Full segments first, then every row's last one: the longest start first.
+  // Every row's last segment, then the full ones (measured on MI355X, us, and the
+  // other way round: 2 rows of 16384 tokens 206, 230; 16 ragged rows of 5003 98,
+  // 102; 32 of 8000 158, 173; 8 of 8000 139, 134).
   if (!lin_unit_head(a, a.more + a.B, unit, h)) return;
   int seg;
-  if (unit < a.more) {
-    if (!lin_full_segment(a, unit, r) || r.err) return;  // reported with the row's last segment
-    seg = unit - r.full0;
+  if (unit >= a.B) {
+    if (!lin_full_segment(a, unit - a.B, r) || r.err) return;  // reported with the row's last segment
+    seg = unit - a.B - r.full0;
   } else {
-    lin_row(a, unit - a.more, r);
+    lin_row(a, unit, r);
     if (r.err) {
       if (r.err > 0 && h == 0 && threadIdx.x == 0 && a.dev_err) atomicOr(a.dev_err, r.err);
       return;
