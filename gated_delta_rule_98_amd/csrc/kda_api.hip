@@ -1,7 +1,7 @@
 // kda_api.hip - the C ABI of include/kda.h, kda_linear.h and kda_norm.h:
 // host-side argument checks, the launch shape from (B, H), and dispatch to the
-// kernel tables of the kernel files. Every entry point validates on the host, then enqueues on the
-// caller's stream; nothing here allocates or synchronizes.
+// kernel tables of the kernel files. Every entry point validates on the host,
+// then enqueues on the caller's stream; nothing here allocates or synchronizes.
 
 #include <string.h>
 
@@ -712,8 +712,13 @@ static void set_lin_tokens(LinArgs &a, const kda_lin_tokens *x, int32_t H) {
   a.group = H / x->Hk;
 }
 
+// A launch takes fewer than 2^31 workgroups and 2^32 threads.
+static bool lin_grid_fits(int64_t blocks, int threads) {
+  return blocks <= 0x7fffffff && blocks * threads <= 0xffffffff;
+}
+
 static int launch_lin(const void *fn, int64_t blocks, int threads, LinArgs &a, void *stream) {
-  if (!fn || blocks > 0x7fffffff) return KDA_ERR_UNSUPPORTED;
+  if (!fn || !lin_grid_fits(blocks, threads)) return KDA_ERR_UNSUPPORTED;
   void *args[] = {&a};
   const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(threads), args, 0, (hipStream_t)stream);
   return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
@@ -739,7 +744,8 @@ int kda_lin_decode_step(float *cache, int64_t num_slots, int64_t slot_stride, co
   const int tile_w = opts ? opts->tile_w : 0;
   if (tile_w == 2) return KDA_ERR_UNSUPPORTED;
   KDA_TRY(choose_width(KIND_DECODE, B, H, dk, dv, epi != nullptr, tile_w, &l));
-  if (l.C == 0) KDA_TRY(choose_width(KIND_DECODE, B, H, dk, dv, false, 4, &l));
+  if (l.C == 0)  // the two-column form of kda_decode_step, which this step does not have
+    KDA_TRY(choose_width(KIND_DECODE, B, H, dk, dv, false, 4, &l));
   if (epi) l = {dv, dv / (4 * kLinGateSlabs), kLinGateSlabs};
 
   a.cache = cache;
@@ -863,10 +869,13 @@ int kda_lin_prefill(float *cache, int64_t num_slots, int64_t slot_stride, const 
   if (n_tok == 0) a.group = 1;  // no tokens, no key heads
   // workgroups for (unit, head), the (unit, key head) pairs dealt to the 8 XCDs
   const auto blocks = [&](int64_t units) { return (units * (H / a.group) + 7) / 8 * 8 * a.group; };
-  if (blocks(B + s.more) > 0x7fffffff) return KDA_ERR_UNSUPPORTED;
+  const int64_t scan_blocks = (int64_t)B * H * lin_scan_parts(dk, dv);
+  // all or nothing is launched
+  if (!lin_grid_fits(blocks(B + s.more), lin_threads(dv)) || (s.more > 0 && !lin_grid_fits(scan_blocks, lin_threads(dv))))
+    return KDA_ERR_UNSUPPORTED;
   if (s.more > 0) {
     KDA_TRY(launch_lin(lin_sum_kernel_for(dk, dv), blocks(s.more), lin_threads(dv), a, stream));
-    KDA_TRY(launch_lin(lin_scan_kernel_for(dk, dv), (int64_t)B * H * lin_scan_parts(dk, dv), lin_threads(dv), a, stream));
+    KDA_TRY(launch_lin(lin_scan_kernel_for(dk, dv), scan_blocks, lin_threads(dv), a, stream));
   }
   return launch_lin(lin_out_kernel_for(dk, dv, a.out_bf16), blocks(B + s.more), lin_threads(dv), a, stream);
 }

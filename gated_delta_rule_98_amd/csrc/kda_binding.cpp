@@ -166,6 +166,14 @@ int64_t integer(PyObject *o) {
   return x;
 }
 
+// While the C entry point runs, other Python threads may.
+struct WithoutGil {
+  PyThreadState *state = PyEval_SaveThread();
+  WithoutGil() = default;
+  WithoutGil(const WithoutGil &) = delete;
+  ~WithoutGil() { PyEval_RestoreThread(state); }
+};
+
 // The stream's handle: None is the current stream of GPU dev.
 void *stream_of(PyObject *o, int dev) {
   PyObject *h;
@@ -233,6 +241,7 @@ PyObject *py_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const kda_options opts = options_of(integer(a[11]), tensor(a[6], "out").scalar_type());
     void *stream = stream_of(a[12], c.dev);
     const c10::DeviceGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)c.dev));
+    const WithoutGil released;
     return lin_decode_step(c.p, c.slots, c.stride, slots, i32(B), i32(c.H), i32(c.dk), i32(c.dv), &x, out,
                            gate ? &epi : nullptr, err, &opts, stream);
   });
@@ -272,6 +281,7 @@ PyObject *py_prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
       // on the current stream's pool: its reuse is ordered behind this call
       if (bytes) ws = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(c10::kCUDA, c.dev));
     }
+    const WithoutGil released;
     return lin_prefill(c.p, c.slots, c.stride, slots, cu, i32(B), i32(n_tok), i32(c.H), i32(c.dk), i32(c.dv), &x, out,
                        pos, ckpt, bytes ? ws.data_ptr() : nullptr, bytes, err, &opts, stream);
   });
@@ -299,6 +309,7 @@ PyObject *py_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const float scale = (float)number(a[6]), eps = (float)number(a[8]);
     void *stream = stream_of(a[9], dev);
     const c10::DeviceGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
+    const WithoutGil released;
     return block_norm(rs.p, rs.stride, static_cast<const uint16_t *>(zs.p), zs.stride, os.p, os.stride, ys.p, ys.stride,
                       wo, static_cast<const uint16_t *>(gs.p), gs.stride, scale, wp, eps, i32(rows), i32(D),
                       (rb ? KDA_NORM_RESID_BF16 : 0) | (yb ? KDA_NORM_Y_BF16 : 0), stream);

@@ -25,9 +25,11 @@
  * the formula gives as long as its products stay in fp32 range. A NaN or an
  * infinity among a row's inputs or in its state reaches outputs and states of
  * that row and head only (in kda_lin_prefill also outputs of up to 63 earlier
- * tokens of the row).
+ * tokens of the row, and an infinity can become a NaN there).
  *
- * Supported shapes: dk, dv in {64, 128}; any H, Hk >= 1 with Hk dividing H.
+ * Supported shapes: dk, dv in {64, 128}; any H, Hk >= 1 with Hk dividing H. A
+ * call whose grid would pass 2^31 workgroups or 2^32 threads is refused
+ * (KDA_ERR_UNSUPPORTED); one of fewer than 2^20 (row, head) pairs fits.
  *
  * Ownership, ordering, errors and device errors are those of kda.h: the library
  * allocates nothing, never synchronizes, and enqueues on `stream`, which must
@@ -70,7 +72,7 @@ int kda_lin_decode_step(float *cache, int64_t num_slots, int64_t slot_stride, co
 /*
  * Packed prompts: row b runs tokens [cu_seqlens[b], cu_seqlens[b+1]) of n_tok
  * (any length, 0 included) from the state in its slot; out gets every token's
- * read-out and the slot the final state. Tokens of out outside every row keep
+ * read-out and the slot the final state. Slot ids must be distinct. Tokens of out outside every row keep
  * their contents. ckpt_pos, ckpt: as for kda_prefill (the state after the first
  * ckpt_pos[b] tokens to ckpt[b], 0 = before the prompt, < 0 = none; past the
  * row is KDA_DEVERR_CKPT). Outputs and states agree with successive

@@ -10,7 +10,9 @@
  * gate the sigmoid is 1, without z r' = r (the first norm of a model), without
  * y only r' is written (the last block). Every intermediate is fp32; y is the
  * norm of the fp32 sum r', also where resid_out rounds it to bf16. The gate is
- * read and applied as kda_epilogue's is.
+ * read and applied as kda_epilogue's is. Squares are fp32 too: a row with values
+ * past about 1e19 overflows its mean square and N is 0 there, or NaN with an
+ * infinity; with eps = 0 a row of zeros gives NaN.
  */
 #ifndef KDA_NORM_H
 #define KDA_NORM_H

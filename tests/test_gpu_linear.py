@@ -1,6 +1,8 @@
 """Linear attention with a decay per head against the plain 64-bit recurrence (linear_ref.py), at the sizes,
 layouts and positions where it can go wrong."""
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -561,3 +563,48 @@ def test_graph_replays_match_eager():
         work()  # eager work between the replays
         torch.cuda.synchronize()
         assert np.array_equal(bits(out), ref[0]), f"eager after replay {r}"
+
+
+def test_two_threads_on_two_streams():
+    """Calls of two threads at once, each on its stream with a workspace of its own, agree with the same calls alone."""
+    dims = [([3000, 70], 4, 2, 128, 128), ([900, 2200], 8, 8, 64, 64)]
+    jobs = []
+    for i, (lens, H, Hk, dk, dv) in enumerate(dims):
+        p = inputs(131 + i, sum(lens), H, Hk, dk, dv, True)
+        q, k, v = (t.to(dev()) for t in split(p, p["x"]))
+        cache0 = cache_of(5 + i, 2, H, dk, dv).to(dev())
+        assert K.kda_lin_prefill_workspace(2, sum(lens), H, dk, dv) > 0
+        jobs.append(dict(cache0=cache0, slots=i32([1, 0]), cu=i32(np.concatenate([[0], np.cumsum(lens)])), q=q, k=k, v=v,
+                         al=p["alpha"].to(dev()), stream=torch.cuda.Stream(),
+                         out=[torch.zeros(sum(lens), H, dv, device=dev()) for _ in range(8)],
+                         cache=[cache0.clone() for _ in range(8)]))
+
+    def run(j, r, stream=None):
+        K.kda_lin_prefill(j["cache"][r], j["slots"], j["cu"], j["q"], j["k"], j["v"], j["al"], j["out"][r], stream=stream)
+        K.kda_lin_decode_step(j["cache"][r], j["slots"], j["q"][:2], j["k"][:2], j["v"][:2], j["al"][:2], j["out"][r][:2],
+                              stream=stream)
+
+    for j in jobs:
+        run(j, 0)
+    torch.cuda.synchronize()
+    log("lin: two threads")
+    failures = []
+
+    def thread(j):
+        try:
+            for r in range(1, 8):
+                run(j, r, j["stream"])
+        except Exception as e:  # noqa: BLE001 - reported by the main thread
+            failures.append(e)
+
+    threads = [threading.Thread(target=thread, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failures, failures
+    for j in jobs:
+        for r in range(1, 8):
+            assert np.array_equal(bits(j["out"][r]), bits(j["out"][0])), r
+            assert np.array_equal(bits(j["cache"][r]), bits(j["cache"][0])), r

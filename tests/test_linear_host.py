@@ -139,6 +139,20 @@ def test_prefill_refusals():
     assert ws(4, 0, 2, 128, 128, ctypes.byref(n)) == E.KDA_OK and n.value == 0
 
 
+@needs_no_gpu
+def test_grids_past_the_launch_limits_are_refused():
+    def opts(w):
+        return ctypes.byref(E.kda_options(w, 0, 0))
+
+    # 2^23 rows x 2 heads x 32 tiles of 64 threads: 2^35 threads; a quarter of 2^32 is launched
+    assert _decode(B=1 << 23, opts=opts(4)) == E.KDA_ERR_UNSUPPORTED
+    assert _decode(B=1 << 18, opts=opts(4)) == E.KDA_ERR_HIP
+    # a workgroup of 512 threads per (row, head)
+    assert _prefill(B=1 << 22) == E.KDA_ERR_UNSUPPORTED
+    assert _prefill(B=(1 << 22) - 4) == E.KDA_ERR_HIP
+    assert _prefill(B=1 << 22, n_tok=0, ckpt_pos=A, ckpt=A) == E.KDA_ERR_UNSUPPORTED
+
+
 def _norm(**over):
     d = dict(resid=A, rs=64, z=A, zs=64, ro=A, ros=64, y=A, ys=64, w_post=A, gate=A, gs=64, scale=1.0, w_pre=A,
              eps=1e-6, rows=3, D=64, flags=0, stream=None)
