@@ -33,7 +33,12 @@ __device__ __forceinline__ void lin_token(float4 (&s)[C][NV], const float4 (&k)[
   for (int c = 0; c < C; ++c) o[c] = row16_sum(o[c]);
 }
 
-// Single-token step, in place: one workgroup per (row, head, W value columns).
+// Single-token step, in place: one workgroup per (row, head, W value columns),
+// the state's 8 bytes per element against 5 operations: HBM-bound with many rows,
+// latency-bound with few. The layout, the widths and their rule are those of
+// kda_decode_step (choose_width); other widths than the rule's were within 3% at
+// best. Measured on MI355X, 32 heads of 128 x 128: 64 rows 45.1 us, 6.0 TB/s (a
+// plain in-place read-modify-write of the same bytes 41.3), one row 3.4.
 template <int DK, int C, bool GATE, bool BF16>
 __global__ __launch_bounds__(256) void lin_decode_kernel(LinArgs a) {
   constexpr int NV = DK / 64;
@@ -561,6 +566,10 @@ __device__ __forceinline__ void tile_decay(const ChunkDecay &d, int st, int tt, 
 }
 
 // ---- the state sum of every segment that another one follows ----
+//
+// Reads k and v once; a wave has 16 columns of the state over all key channels
+// in accumulators. 8000 tokens x 32 heads of 128 x 128: 44 us for 126 MB read and
+// 31 written (3.6 TB/s); two rows of 16384 x 32 of 64 x 64: 66 us for 242 and 7.
 template <int DK, int DV>
 __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_sum_kernel(LinArgs a) {
   constexpr int NT = lin_threads(DV), NW = NT / 64;
@@ -620,6 +629,11 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_sum_kernel(L
 }
 
 // ---- the state entering every segment of a row, in place of the sums ----
+//
+// A thread takes 4 elements through the row's segments. One row of 15 full
+// segments x 32 heads of 128 x 128: 13 us, a chain of loads from the Infinity
+// Cache; 16 ragged rows of 5003 tokens in all 13 us (a workgroup for every row and
+// head, most of them of rows that are not cut).
 template <int DK, int DV>
 __global__ __launch_bounds__(lin_threads(DV)) void lin_scan_kernel(LinArgs a) {
   int bh, ni, b, h;
@@ -643,6 +657,16 @@ __global__ __launch_bounds__(lin_threads(DV)) void lin_scan_kernel(LinArgs a) {
 }
 
 // ---- outputs, final state and checkpoint ----
+//
+// 8000 tokens x 32 heads of 128 x 128, fp32 out: 90 to 105 us with the clock (84
+// where it is 100 if every chunk's inputs are resident in L2), so what bounds it is
+// mostly not HBM. A chunk of one head takes a wave 48 MFMAs for S0^T q, 5 for the
+// scores, 18 for their product with v and 48 for the state, and as many cycles of
+// VALU work to split the fp32 operands, in phases that barriers keep apart: MFMA
+// and VALU are busy about a third of the time each. 8 waves of 16 columns keep 128
+// registers and so two workgroups per CU; 4 waves of 32 columns spilled (137 us).
+// Bank conflicts count little: with the transposing reads' two rows apart, which
+// takes a fifth of them away, the times were the same within 1%.
 template <int DK, int DV, bool BF16>
 __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(LinArgs a) {
   constexpr int NT = lin_threads(DV), NW = NT / 64, KB = DK / 32, T = kLinChunk / kLB;
@@ -654,9 +678,10 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
   __shared__ __align__(16) ChunkDecay dec[NW];  // of a group of NW chunks
   int unit, h;
   LinRow r;
-  // Every row's last segment, then the full ones (measured on MI355X, us, and the
-  // other way round: 2 rows of 16384 tokens 206, 230; 16 ragged rows of 5003 98,
-  // 102; 32 of 8000 158, 173; 8 of 8000 139, 134).
+  // Every row's last segment, then the full ones (measured on MI355X, the whole
+  // prefill of 32 heads, us, and the other way round: 2 rows of 16384 tokens x
+  // 64 x 64 206, 230; 16 ragged rows of 5003 tokens in all 98, 102; 32 of 8000
+  // 158, 173; 8 of 8000 139, 134).
   if (!lin_unit_head(a, a.more + a.B, unit, h)) return;
   int seg;
   if (unit >= a.B) {
@@ -813,8 +838,8 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
 // Short prompts of few heads: a workgroup per 16 value columns
 // ----------------------------------------------------------------------------
 //
-// With few (row, head) pairs the kernel above leaves most CUs idle and a chunk
-// takes it 5 us. Here a workgroup has 16 columns of a head and walks the whole
+// With few (row, head) pairs the kernel above leaves most CUs idle, and latency
+// is what counts. Here a workgroup has 16 columns of a head and walks the whole
 // row, its waves in two roles, one barrier per chunk. DK / 32 waves carry the
 // state: S0^T q_t over the wave's 32 channels, to LDS, then the update. Six waves
 // take the scores' products with v, up to 2 score tiles each, split in registers
@@ -822,7 +847,9 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
 // ones. One chunk later four of them add up their tokens' terms and write.
 // A chunk is requested two chunks ahead (two register sets rotate) and written to
 // LDS one ahead. Every column tile forms the scores again, so this costs more
-// work in total than the kernel above; lin_walks (kda_api.hip) says where it wins.
+// work in total than the kernel above (8000 tokens x 32 heads: 337 us); lin_walks
+// (kda_api.hip) says where it wins. 37 tokens x 32 heads of 128 x 128: 7.0 us
+// (the kernel above 11.3), a chunk more takes 2.5 us.
 
 constexpr int kWalkTile = 16, kWalkOutWaves = 6;
 
