@@ -608,3 +608,58 @@ def test_two_threads_on_two_streams():
         for r in range(1, 8):
             assert np.array_equal(bits(j["out"][r]), bits(j["out"][0])), r
             assert np.array_equal(bits(j["cache"][r]), bits(j["cache"][0])), r
+
+
+def test_streams_by_handle():
+    """`stream` as an integer handle, the default stream's 0 among them, with the call's own workspace."""
+    lens = [2000, 3]
+    p = inputs(141, sum(lens), 4, 4, 128, 64, False)
+    cache0 = cache_of(6, 2, 4, 64, 128)
+    slots = np.array([0, 1], np.int32)
+    ref = run_prefill(p, lens, slots, cache0)
+    side = torch.cuda.Stream()
+    for handle in (torch.cuda.default_stream().cuda_stream, side.cuda_stream):
+        torch.cuda.synchronize()
+        log(f"lin: stream handle {'0' if handle == 0 else 'of a side stream'}")
+        side.wait_stream(torch.cuda.current_stream())
+        # the inputs are copied on the current stream: ordered before the side stream's work
+        q, k, v = split(p, p["x"].to(dev()))
+        cache, out = cache0.to(dev()), sentinel((sum(lens), 4, 64))
+        al, s, cu = p["alpha"].to(dev()), i32(slots), i32([0, 2000, 2003])
+        torch.cuda.synchronize()
+        K.kda_lin_prefill(cache, s, cu, q, k, v, al, out, stream=handle)
+        torch.cuda.synchronize()
+        assert np.array_equal(bits(out), bits(ref[0])) and np.array_equal(bits(cache), bits(ref[1]))
+
+
+def test_two_graphs_that_share_a_memory_pool():
+    """Two graphs captured into one pool, each allocating its call's workspace there, replayed in turn."""
+    jobs = []
+    for i, lens in enumerate(([1500, 10], [700, 900])):
+        p = inputs(151 + i, sum(lens), 4, 2, 128, 128, True)
+        q, k, v = (t.to(dev()) for t in split(p, p["x"]))
+        cache0 = cache_of(8 + i, 2, 4, 128, 128).to(dev())
+        assert K.kda_lin_prefill_workspace(2, sum(lens), 4, 128, 128) > 0
+        j = dict(cache0=cache0, cache=cache0.clone(), out=torch.zeros(sum(lens), 4, 128, device=dev()),
+                 args=(i32([1, 0]), i32([0, lens[0], sum(lens)]), q, k, v, p["alpha"].to(dev())))
+        K.kda_lin_prefill(j["cache"], *j["args"], j["out"])
+        torch.cuda.synchronize()
+        j["ref"] = bits(j["out"]), bits(j["cache"])
+        jobs.append(j)
+    pool = torch.cuda.graph_pool_handle()
+    for j in jobs:
+        j["graph"] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(j["graph"], pool=pool):
+            K.kda_lin_prefill(j["cache"], *j["args"], j["out"])
+    for r in range(3):
+        log(f"lin: shared pool, replay {r}")
+        for j in jobs:
+            j["cache"].copy_(j["cache0"])
+            j["out"].zero_()
+        for j in jobs if r % 2 else jobs[::-1]:
+            j["graph"].replay()
+        torch.cuda.synchronize()
+        for j in jobs:
+            assert np.array_equal(bits(j["out"]), j["ref"][0]) and np.array_equal(bits(j["cache"]), j["ref"][1]), r
+        K.kda_lin_prefill(jobs[0]["cache"], *jobs[0]["args"], jobs[0]["out"])  # eager work between the replays
+        torch.cuda.synchronize()
