@@ -118,9 +118,10 @@ __global__ __launch_bounds__(256) void lin_decode_kernel(LinArgs a) {
 // in bfloat16. The other operand of a product (the state, the decayed scores,
 // the tokens scaled to the chunk's end) is fp32 and is split by truncation into
 // three bfloat16 parts, 8 + 8 + 8 bits of its 24, which is exact; the three
-// products are exact in fp32 and accumulate there. Where only outputs that are
-// then rounded to bfloat16 (2^-9) depend on it, two parts rounded to nearest
-// do: 2^-18 of each term, a third fewer products.
+// products are exact in fp32 and accumulate there. A bfloat16 output is the fp32
+// one rounded once, so it takes all three parts too. (Two, 2^-18 of each term,
+// moved one output in 400 to a neighbouring bfloat16; 16 ragged rows 98 us, 107 with
+// three, 2 rows of 16384 x 64 x 64 211 and 223, 37 tokens the same.)
 //
 // A checkpoint cuts its row's chunks: the one that reaches it ends there, so
 // the state there falls on a chunk's edge.
@@ -140,8 +141,7 @@ __device__ __forceinline__ int score_row(int tt, int m) {  // element of row 16 
   return tt < 2 ? (kLB * tt + m) * 40 : 32 * 40 + (kLB * (tt - 2) + m) * 72;
 }
 
-template <bool BF16>
-constexpr int kOutParts = BF16 ? 2 : 3;  // of an fp32 operand of the output products
+constexpr int kParts = 3;  // bfloat16 parts of an fp32 operand
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -149,7 +149,6 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // (x0, x1) - (the word's two bfloat16), exact where they are the parts of x0 and
 // x1 below: one dot-product instruction each. The factors (-1, 0) and (0, -1) are
@@ -169,36 +168,30 @@ __device__ __forceinline__ uint32_t upper_pair(float x0, float x1) {
 }
 
 // The bfloat16 parts of x, largest first, part i in words [i N/2, (i + 1) N/2):
-// three by truncation (8 bits of the 24 each, exact), or two rounded to nearest
-// (x to within 2^-18 of it).
-template <int PARTS, int N>
-__device__ __forceinline__ void split_words(const float (&x)[N], uint32_t (&w)[PARTS * N / 2]) {
+// by truncation, 8 bits of the 24 each.
+template <int N>
+__device__ __forceinline__ void split_words(const float (&x)[N], uint32_t (&w)[kParts * N / 2]) {
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) {
     float x0 = x[2 * i], x1 = x[2 * i + 1];
 #pragma unroll
-    for (int part = 0; part < PARTS; ++part) {
+    for (int part = 0; part < kParts; ++part) {
       uint32_t &h = w[part * N / 2 + i];
-      if constexpr (PARTS == 3)
-        h = upper_pair(x0, x1);
-      else
-        h = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){x0, x1}, bf16x2));
-      if (part + 1 < PARTS) minus_pair(h, x0, x1);
+      h = upper_pair(x0, x1);
+      if (part + 1 < kParts) minus_pair(h, x0, x1);
     }
   }
 }
 
-template <int PARTS>
 struct Split {
-  bf16x8 part[PARTS];
+  bf16x8 part[kParts];
 };
-template <int PARTS>
-__device__ __forceinline__ Split<PARTS> split(const float (&x)[8]) {
-  uint32_t w[PARTS * 4];
-  split_words<PARTS, 8>(x, w);
-  Split<PARTS> r;
+__device__ __forceinline__ Split split(const float (&x)[8]) {
+  uint32_t w[kParts * 4];
+  split_words<8>(x, w);
+  Split r;
 #pragma unroll
-  for (int i = 0; i < PARTS; ++i)
+  for (int i = 0; i < kParts; ++i)
     r.part[i] = __builtin_bit_cast(bf16x8, (u32x4){w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]});
   return r;
 }
@@ -484,7 +477,7 @@ struct Staged16 {
 };
 
 // Tokens 32 kb + 8 g .. + 7 of a column, each times its factor f, split.
-__device__ __forceinline__ Split<3> scaled_values(bf16x8 v, const float (&f)[8]) {
+__device__ __forceinline__ Split scaled_values(bf16x8 v, const float (&f)[8]) {
   const u32x4 u = __builtin_bit_cast(u32x4, v);
   float x[8];
 #pragma unroll
@@ -492,7 +485,7 @@ __device__ __forceinline__ Split<3> scaled_values(bf16x8 v, const float (&f)[8])
     x[2 * e] = __uint_as_float(u[e] << 16) * f[2 * e];
     x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u) * f[2 * e + 1];
   }
-  return split<3>(x);
+  return split(x);
 }
 
 // S <- Gamma_L S + sum_s end_s k_s v_s^T
@@ -509,14 +502,14 @@ __device__ __forceinline__ void chunk_state(LinState<DK, DV> &S, const uint16_t 
     float f[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = d.end[32 * kb + 8 * g + e];
-    const Split<3> vs = scaled_values(vr[kb], f);
+    const Split vs = scaled_values(vr[kb], f);
 #pragma unroll
     for (int n4 = 0; n4 < NI; n4 += 4) {
       bf16x8 kt[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) kt[i] = ld_tokens<DK + 8>(kl, 32 * kb, 16 * (n4 + i));
 #pragma unroll
-      for (int x = 2; x >= 0; --x)
+      for (int x = kParts - 1; x >= 0; --x)
 #pragma unroll
         for (int i = 0; i < 4; ++i) S.s[n4 + i] = mma(kt[i], vs.part[x], S.s[n4 + i]);
     }
@@ -670,11 +663,10 @@ __global__ __launch_bounds__(lin_threads(DV)) void lin_scan_kernel(LinArgs a) {
 template <int DK, int DV, bool BF16>
 __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(LinArgs a) {
   constexpr int NT = lin_threads(DV), NW = NT / 64, KB = DK / 32, T = kLinChunk / kLB;
-  constexpr int PARTS = kOutParts<BF16>;
   __shared__ __align__(16) uint16_t ql[kLinChunk * (DK + 8)];
   __shared__ __align__(16) uint16_t kl[kLinChunk * (DK + 8)];
   __shared__ __align__(16) uint16_t vl[kLinChunk * (DV + 8)];
-  __shared__ __align__(16) uint16_t pl[PARTS][kScoreElems];  // decayed scores, split
+  __shared__ __align__(16) uint16_t pl[kParts][kScoreElems];  // decayed scores, split
   __shared__ __align__(16) ChunkDecay dec[NW];  // of a group of NW chunks
   int unit, h;
   LinRow r;
@@ -716,7 +708,7 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
   const uint16_t *v = a.v + tok0 * a.vs + (int64_t)h * DV;
   const float *al = a.alpha + tok0 * a.as + h;
   // the tiles above the diagonal that a product over 32 tokens reads: (1, 0) and (3, 2)
-  for (int i = threadIdx.x; i < PARTS * 2 * kLB * kLB / 4; i += NT) {
+  for (int i = threadIdx.x; i < kParts * 2 * kLB * kLB / 4; i += NT) {
     const int part = i >> 7, up = (i >> 6) & 1, t = (i >> 2) & 15, s = (i & 3) * 4;
     *reinterpret_cast<u32x2 *>(&pl[part][score_row(2 * up, t) + 32 * up + kLB + s]) = (u32x2){0u, 0u};
   }
@@ -765,10 +757,10 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
       tile_decay(d, st, tt, D);
 #pragma unroll
       for (int e = 0; e < 4; ++e) p[e] = st < tt || m >= 4 * g + e ? acc[e] * D[e] : 0.0f;
-      uint32_t w[2 * PARTS];
-      split_words<PARTS, 4>(p, w);
+      uint32_t w[2 * kParts];
+      split_words<4>(p, w);
 #pragma unroll
-      for (int x = 0; x < PARTS; ++x)
+      for (int x = 0; x < kParts; ++x)
         *reinterpret_cast<u32x2 *>(&pl[x][score_row(tt, m) + kLB * st + 4 * g]) = (u32x2){w[2 * x], w[2 * x + 1]};
     }
 
@@ -781,13 +773,13 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
       float x[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = S.s[2 * kb + e / 4][e % 4];
-      const Split<PARTS> sp = split<PARTS>(x);
+      const Split sp = split(x);
 #pragma unroll
       for (int t2 = 0; t2 < T; t2 += 2) {
         const bf16x8 q0 = ld_run4x2(ql + (kLB * t2 + m) * (DK + 8) + 32 * kb + 4 * g);
         const bf16x8 q1 = ld_run4x2(ql + (kLB * (t2 + 1) + m) * (DK + 8) + 32 * kb + 4 * g);
 #pragma unroll
-        for (int i = PARTS - 1; i >= 0; --i) {
+        for (int i = kParts - 1; i >= 0; --i) {
           o[t2] = mma(sp.part[i], q0, o[t2]);
           o[t2 + 1] = mma(sp.part[i], q1, o[t2 + 1]);
         }
@@ -802,7 +794,7 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-      for (int x = PARTS - 1; x >= 0; --x)
+      for (int x = kParts - 1; x >= 0; --x)
 #pragma unroll
         for (int tt = 2 * kb; tt < T; ++tt)
           o[tt] = mma(vr[kb], ld_run8(&pl[x][score_row(tt, m) + 32 * kb + 8 * g]), o[tt]);
@@ -940,7 +932,7 @@ struct WaveState {
   __device__ __forceinline__ void update(const WalkTokens<DK> &x, const ChunkDecay &d, int r) {
     const int g = (threadIdx.x & 63) >> 4;
     bf16x8 kt[2][2];
-    Split<3> vs[2];
+    Split vs[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
@@ -955,7 +947,7 @@ struct WaveState {
     s[0] *= gl;
     s[1] *= gl;
 #pragma unroll
-    for (int x = 2; x >= 0; --x)
+    for (int x = kParts - 1; x >= 0; --x)
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
         s[0] = mma(kt[kb][0], vs[kb].part[x], s[0]);
@@ -967,7 +959,6 @@ struct WaveState {
 template <int DK, bool BF16>
 __global__ __launch_bounds__(lin_walk_threads(DK)) void lin_walk_kernel(LinArgs a) {
   constexpr int NR = DK / 32, NW = NR + kWalkOutWaves, PITCH = DK + 8, T = kLinChunk / kLB;
-  constexpr int PARTS = kOutParts<BF16>;
   __shared__ __align__(16) WalkTokens<DK> tok[2];
   __shared__ __align__(16) ChunkDecay dec[2];
   __shared__ v4f part[2][NR][T][64];  // state terms by (chunk parity, wave, 16 tokens)
@@ -1030,7 +1021,7 @@ __global__ __launch_bounds__(lin_walk_threads(DK)) void lin_walk_kernel(LinArgs 
     const auto step = [&](int c, int p) {
       load(c + 2, p);
       const float xs[8] = {S.s[0][0], S.s[0][1], S.s[0][2], S.s[0][3], S.s[1][0], S.s[1][1], S.s[1][2], S.s[1][3]};
-      const Split<PARTS> sp = split<PARTS>(xs);
+      const Split sp = split(xs);
       bf16x8 qv[T];
 #pragma unroll
       for (int tt = 0; tt < T; ++tt) qv[tt] = ld_run4x2(tok[p].q + (kLB * tt + m) * PITCH + 32 * wave + 4 * g);
@@ -1038,7 +1029,7 @@ __global__ __launch_bounds__(lin_walk_threads(DK)) void lin_walk_kernel(LinArgs 
 #pragma unroll
       for (int tt = 0; tt < T; ++tt) o[tt] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int i = PARTS - 1; i >= 0; --i)
+      for (int i = kParts - 1; i >= 0; --i)
 #pragma unroll
         for (int tt = 0; tt < T; ++tt) o[tt] = mma(sp.part[i], qv[tt], o[tt]);
 #pragma unroll
@@ -1108,11 +1099,11 @@ __global__ __launch_bounds__(lin_walk_threads(DK)) void lin_walk_kernel(LinArgs 
 #pragma unroll
       for (int e = 0; e < 4; ++e) ps[4 * i + e] = st < tt || (st == tt && m >= 4 * g + e) ? sc[e] * D[e] : 0.0f;
     }
-    const Split<PARTS> sp = split<PARTS>(ps);
+    const Split sp = split(ps);
     const bf16x8 vv = ld_tokens2<kWalkTile>(tok[p].v, 32 * kb, 0);
     acc = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = PARTS - 1; i >= 0; --i) acc = mma(vv, sp.part[i], acc);
+    for (int i = kParts - 1; i >= 0; --i) acc = mma(vv, sp.part[i], acc);
     if (!writes) early[p][3 - tt][lane] = acc;
     put(c + 1, p ^ 1);
     __syncthreads();
