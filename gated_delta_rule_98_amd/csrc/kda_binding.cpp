@@ -27,7 +27,8 @@ decltype(&kda_lin_decode_step) lin_decode_step;
 decltype(&kda_lin_prefill) lin_prefill;
 decltype(&kda_lin_prefill_workspace) lin_prefill_workspace;
 decltype(&kda_block_norm) block_norm;
-PyObject *raw_stream;  // torch: device index -> handle of its current stream
+PyObject *raw_stream;    // torch: device index -> handle of its current stream
+PyObject *workspace_on;  // kda.py: (bytes, device index, stream) -> tensor allocated on that stream
 
 struct PythonError {};  // a Python exception is set
 
@@ -194,6 +195,15 @@ void *stream_of(PyObject *o, int dev) {
   return p;
 }
 
+// A workspace allocated on a stream that the caller named.
+at::Tensor workspace(size_t bytes, int dev, PyObject *stream) {
+  PyObject *t = PyObject_CallFunction(workspace_on, "niO", (Py_ssize_t)bytes, dev, stream);
+  if (!t) throw PythonError();
+  const at::Tensor r = THPVariable_Unpack(t);
+  Py_DECREF(t);
+  return r;
+}
+
 template <class F>
 PyObject *guarded(F &&f) {
   try {
@@ -278,8 +288,11 @@ PyObject *py_prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
     } else {
       const int rc = lin_prefill_workspace(i32(B), i32(n_tok), i32(c.H), i32(c.dk), i32(c.dv), &bytes);
       if (rc != KDA_OK) return rc;
-      // on the current stream's pool: its reuse is ordered behind this call
-      if (bytes) ws = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(c10::kCUDA, c.dev));
+      // allocated on the stream that uses it, so that its reuse is ordered behind this call
+      if (bytes && a[12] == Py_None)
+        ws = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(c10::kCUDA, c.dev));
+      else if (bytes)
+        ws = workspace(bytes, c.dev, a[12]);
     }
     const WithoutGil released;
     return lin_prefill(c.p, c.slots, c.stride, slots, cu, i32(B), i32(n_tok), i32(c.H), i32(c.dk), i32(c.dv), &x, out,
@@ -317,10 +330,10 @@ PyObject *py_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 // The entry points' addresses (kda_lin_decode_step, kda_lin_prefill,
-// kda_lin_prefill_workspace, kda_block_norm) and torch's stream lookup.
+// kda_lin_prefill_workspace, kda_block_norm), torch's stream lookup and workspace_on.
 PyObject *py_bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> int {
-    expect(n, 5);
+    expect(n, 6);
     const auto address = [&](int i) {
       void *p = PyLong_AsVoidPtr(a[i]);
       if (!p) throw ValueError("null entry point");
@@ -332,6 +345,8 @@ PyObject *py_bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     block_norm = reinterpret_cast<decltype(block_norm)>(address(3));
     Py_INCREF(a[4]);
     Py_XSETREF(raw_stream, a[4]);
+    Py_INCREF(a[5]);
+    Py_XSETREF(workspace_on, a[5]);
     return 0;
   });
 }

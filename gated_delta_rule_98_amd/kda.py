@@ -194,6 +194,23 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def workspace_on(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace of the device, allocated on `stream` (a torch stream or a handle; None: the current one). The
+    caching allocator hands a freed block to later work of the stream it was allocated on, so a workspace has to
+    come from the stream that uses it: its reuse is then ordered behind the call."""
+    def empty():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+    if stream is None:
+        return empty()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        # ExternalStream takes 0 for "no handle given" and returns a stream of torch's pool
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return empty()
+
+
 def _epilogue(gate, weight, eps):
     if gate is None:
         return None

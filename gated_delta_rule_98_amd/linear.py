@@ -56,15 +56,8 @@ def kda_lin_prefill(cache: torch.Tensor, slot_ids: torch.Tensor, cu_seqlens: tor
     """Whole prompts with an optional in-pass checkpoint. Token arrays are as for kda_lin_decode_step
     with n_tok tokens; row b owns tokens [cu_seqlens[b], cu_seqlens[b + 1]); ckpt_pos int32 [B], ckpt
     float32 [B, H, dv, dk]. workspace: a contiguous tensor of any dtype, at least
-    kda_lin_prefill_workspace() bytes; None allocates one for the call."""
-    if workspace is None and stream is not None:
-        # allocated on the stream that uses it, so that its reuse is ordered behind the call
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=cache.device)):
-            rc = native().lin_prefill(cache, slot_ids, cu_seqlens, q, k, v, alpha, out, ckpt_pos, ckpt, None,
-                                      dev_err, handle)
-    else:
-        rc = native().lin_prefill(cache, slot_ids, cu_seqlens, q, k, v, alpha, out, ckpt_pos, ckpt, workspace,
-                                  dev_err, stream)
+    kda_lin_prefill_workspace() bytes; None allocates one for the call, on the stream that it runs on."""
+    rc = native().lin_prefill(cache, slot_ids, cu_seqlens, q, k, v, alpha, out, ckpt_pos, ckpt, workspace, dev_err,
+                              stream)
     if rc != KDA_OK:
         raise KdaError(rc, "kda_lin_prefill")

@@ -11,7 +11,7 @@ import os
 
 import torch
 
-from .kda import load_library
+from .kda import load_library, workspace_on
 
 PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "kda_native.so")
 
@@ -33,6 +33,6 @@ def native():
             (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
         mod.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                    for f in ("kda_lin_decode_step", "kda_lin_prefill", "kda_lin_prefill_workspace",
-                             "kda_block_norm")), stream)
+                             "kda_block_norm")), stream, workspace_on)
         _module = mod
     return _module

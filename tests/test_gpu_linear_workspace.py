@@ -1,0 +1,61 @@
+"""Workspaces of kda_lin_prefill on the GPU: the stream they are allocated on."""
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_98_amd as K
+from gpu_util import bits, dev, i32, log
+from test_gpu_linear import cache_of, inputs, split
+
+pytestmark = pytest.mark.gpu
+
+
+def long_prompt(seed, n=4000, H=32):
+    """Arguments of a call whose workspace is too large for any other tensor's leftover block."""
+    p = inputs(seed, n, H, 1, 128, 128, False)
+    q, k, v = split(p, p["x"].to(dev()))
+    args = (cache_of(seed, 1, H, 128, 128).to(dev()), i32([0]), i32([0, n]), q, k, v, p["alpha"].to(dev()),
+            torch.empty(n, H, 128, device=dev()))
+    need = K.kda_lin_prefill_workspace(1, n, H, 128, 128)
+    return args, need
+
+
+@pytest.mark.parametrize("kind", ["none", "handle 0", "default stream", "current stream", "side stream", "side handle"])
+def test_workspace_comes_from_the_stream_of_the_launch(kind):
+    args, need = long_prompt(171)
+    assert need >= 32 << 20
+    side = torch.cuda.Stream()
+    stream, handle = {"none": (None, 0), "handle 0": (0, 0), "default stream": (torch.cuda.default_stream(), 0),
+                      "current stream": (torch.cuda.current_stream(), 0), "side stream": (side, side.cuda_stream),
+                      "side handle": (side.cuda_stream, side.cuda_stream)}[kind]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    before = {s["address"] for s in torch.cuda.memory_snapshot()}
+    log(f"lin prefill on stream {kind}")
+    K.kda_lin_prefill(*args, stream=stream)
+    torch.cuda.synchronize()
+    new = [s for s in torch.cuda.memory_snapshot() if s["address"] not in before]
+    assert sum(s["total_size"] for s in new) >= need
+    assert {s["stream"] for s in new} == {handle}
+    torch.cuda.empty_cache()
+
+
+def test_calls_on_the_default_stream_and_on_pool_streams_at_once():
+    """Calls on handle 0 and on 32 streams of torch's pool, each with a workspace of the call's own, queued without a
+    wait between them, agree with the calls alone."""
+    args, _ = long_prompt(181, 2100, 16)
+    cache0 = args[0].clone()
+    K.kda_lin_prefill(*args)
+    torch.cuda.synchronize()
+    ref = bits(args[0]), bits(args[7])
+    streams = [torch.cuda.Stream() for _ in range(32)]
+    caches = [cache0.clone() for _ in range(33)]
+    outs = [torch.empty_like(args[7]) for _ in range(33)]
+    torch.cuda.synchronize()
+    log("lin prefill on 33 streams")
+    for c, o, s in zip(caches, outs, [0] + streams):
+        K.kda_lin_prefill(c, *args[1:7], o, stream=s)
+    torch.cuda.synchronize()
+    for i, (c, o) in enumerate(zip(caches, outs)):
+        assert np.array_equal(bits(c), ref[0]) and np.array_equal(bits(o), ref[1]), i

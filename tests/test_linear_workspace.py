@@ -1,0 +1,57 @@
+"""Workspaces of the linear-attention calls on the host: the stream they are allocated on."""
+
+import contextlib
+
+import pytest
+import torch
+
+import gated_delta_rule_98_amd.linear as linear
+from gated_delta_rule_98_amd import kda
+
+
+class Stream:
+    def __init__(self, cuda_stream):
+        self.cuda_stream = cuda_stream
+
+
+@pytest.fixture
+def cuda(monkeypatch):
+    """torch.cuda's stream functions without a GPU; entered: the handles of the streams made current, in order."""
+    entered = []
+
+    def external(handle, device=None):
+        assert handle != 0, "ExternalStream(0) is a stream of torch's pool, not the default stream"
+        return Stream(handle)
+
+    @contextlib.contextmanager
+    def current(s):
+        entered.append(s.cuda_stream)
+        yield
+
+    monkeypatch.setattr(torch.cuda, "ExternalStream", external)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: Stream(0))
+    monkeypatch.setattr(torch.cuda, "stream", current)
+    return entered
+
+
+@pytest.mark.parametrize("stream", [0, Stream(0), 64, Stream(64)], ids=["0", "stream 0", "64", "stream 64"])
+def test_prefill_builds_no_stream_from_handle_zero(cuda, monkeypatch, stream):
+    class Native:
+        @staticmethod
+        def lin_prefill(*args):
+            return kda.KDA_OK
+
+    monkeypatch.setattr(linear, "native", Native)
+    linear.kda_lin_prefill(torch.zeros(1), *[None] * 7, stream=stream)
+
+
+@pytest.mark.parametrize("stream,handle", [(0, 0), (Stream(0), 0), (64, 64), (Stream(64), 64)],
+                         ids=["0", "stream 0", "64", "stream 64"])
+def test_workspace_is_allocated_on_the_stream_that_uses_it(cuda, stream, handle):
+    assert kda.workspace_on(24, "cpu", stream).nbytes == 24
+    assert cuda == [handle]
+
+
+def test_workspace_without_a_stream_stays_on_the_current_one(cuda):
+    assert kda.workspace_on(24, "cpu", None).nbytes == 24
+    assert cuda == []
