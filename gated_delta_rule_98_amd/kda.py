@@ -425,12 +425,11 @@ def kda_prefill_chunked(cache: torch.Tensor, slot_ids: torch.Tensor, cu_seqlens:
                         dev_err: Optional[torch.Tensor] = None, tile_w: int = 0, raw_inputs: bool = False,
                         stream=None) -> None:
     """Chunk form of kda_prefill: same arguments plus a device workspace (any dtype, at least
-    kda_prefill_chunked_workspace() bytes); None allocates one for the call."""
+    kda_prefill_chunked_workspace() bytes); None allocates one for the call, on the stream that it runs on."""
     B, n_tok, H, dk, dv, ns, stride = _prefill_chunked_checks(cache, slot_ids, cu_seqlens, q, k, v, alpha, beta,
                                                               out, ckpt_pos, ckpt, dev_err)
     if workspace is None:
-        workspace = torch.empty(kda_prefill_chunked_workspace(B, n_tok, H, dk, dv), dtype=torch.uint8,
-                                device=cache.device)
+        workspace = workspace_on(kda_prefill_chunked_workspace(B, n_tok, H, dk, dv), cache.device, stream)
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous device tensor")
     rc = load_library().kda_prefill_chunked(

@@ -1,4 +1,4 @@
-"""Workspaces of kda_lin_prefill on the GPU: the stream they are allocated on."""
+"""Workspaces of the prefill calls on the GPU: the stream they are allocated on."""
 
 import numpy as np
 import pytest
@@ -59,3 +59,21 @@ def test_calls_on_the_default_stream_and_on_pool_streams_at_once():
     torch.cuda.synchronize()
     for i, (c, o) in enumerate(zip(caches, outs)):
         assert np.array_equal(bits(c), ref[0]) and np.array_equal(bits(o), ref[1]), i
+
+
+def test_chunk_prefill_workspace_comes_from_the_stream_of_the_launch():
+    n, H, d = 2000, 32, 128
+    assert K.kda_prefill_chunked_workspace(1, n, H, d, d) >= 32 << 20
+    x = torch.full((n, H, d), 0.05, dtype=torch.bfloat16, device=dev())
+    args = (torch.zeros(1, H, d, d, device=dev()), i32([0]), i32([0, n]), x, x, x, torch.full((n, H, d), 0.9, device=dev()),
+            torch.full((n, H), 0.5, device=dev()), torch.empty(n, H, d, device=dev()))
+    side = torch.cuda.Stream()
+    for stream, handle in ((0, 0), (side, side.cuda_stream)):
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        before = {s["address"] for s in torch.cuda.memory_snapshot()}
+        log(f"chunk prefill on stream handle {'0' if handle == 0 else 'of a side stream'}")
+        K.kda_prefill_chunked(*args, stream=stream)
+        torch.cuda.synchronize()
+        assert {s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] not in before} == {handle}
+    torch.cuda.empty_cache()

@@ -1,4 +1,4 @@
-"""Workspaces of the linear-attention calls on the host: the stream they are allocated on."""
+"""Workspaces of the prefill calls on the host: the stream they are allocated on."""
 
 import contextlib
 
@@ -55,3 +55,12 @@ def test_workspace_is_allocated_on_the_stream_that_uses_it(cuda, stream, handle)
 def test_workspace_without_a_stream_stays_on_the_current_one(cuda):
     assert kda.workspace_on(24, "cpu", None).nbytes == 24
     assert cuda == []
+
+
+@pytest.mark.parametrize("stream,handle", [(None, None), (0, 0), (Stream(64), 64)], ids=["none", "0", "stream 64"])
+def test_chunk_prefill_allocates_on_the_stream_that_uses_it(cuda, monkeypatch, stream, handle):
+    monkeypatch.setattr(kda, "_prefill_chunked_checks", lambda *a: (1, 8, 1, 64, 64, 1, 4096))
+    monkeypatch.setattr(kda, "kda_prefill_chunked_workspace", lambda *a: 24)
+    with pytest.raises(ValueError, match="device tensor"):  # a host workspace goes no further
+        kda.kda_prefill_chunked(torch.zeros(1), *[None] * 8, stream=stream)
+    assert cuda == ([] if handle is None else [handle])
