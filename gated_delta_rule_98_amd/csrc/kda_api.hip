@@ -797,20 +797,30 @@ struct LinSplit {
 static LinSplit lin_split(int32_t B, int32_t n_tok, int32_t H) {
   const int64_t chunks = n_tok / kLinChunk;
   const int64_t few = chunks < 4 * (int64_t)B ? 4 : std::min<int64_t>(4, std::max<int64_t>(2, (chunks * H + 255) / 256));
-  const int64_t seg = std::min<int64_t>(std::max<int64_t>(few, ((chunks + B) * H + 511) / 512), 1 << 24);
+  const int64_t seg = std::min<int64_t>(std::max<int64_t>(few, ((chunks + B) * H + 511) / 512), chunks + 1);
   return {(int32_t)seg, n_tok > 0 ? (n_tok - 1) / kLinChunk / seg : 0};
 }
 
-static size_t lin_ws_state_bytes(const LinSplit &s, int32_t H, int32_t dk, int32_t dv) {
-  return (size_t)(2 * s.more) * H * dk * dv * sizeof(float);
+// A state for every segment of a row that has two or more, of `more` segments
+// that another one follows.
+static size_t lin_ws_state_bytes(int64_t more, int32_t H, int32_t dk, int32_t dv) {
+  return (size_t)(2 * more) * H * dk * dv * sizeof(float);
 }
 
 int kda_lin_prefill_workspace(int32_t B, int32_t n_tok, int32_t H, int32_t dk, int32_t dv, size_t *bytes) {
   if (!bytes || B < 0 || n_tok < 0 || H <= 0 || dk <= 0 || dv <= 0) return KDA_ERR_INVALID;
   if (!dims_supported(dk, dv)) return KDA_ERR_UNSUPPORTED;
-  const LinSplit s = lin_walks(B, n_tok, H, dv) ? LinSplit{0, 0} : lin_split(B, n_tok, H);
-  // a state for every segment of a row that has two or more, then their decays
-  *bytes = lin_ws_state_bytes(s, H, dk, dv) + ((size_t)(2 * s.more) * H * sizeof(float) + 15) / 16 * 16;
+  int64_t more = 0;
+  if (!lin_walks(B, n_tok, H, dv) && n_tok > 0) {
+    // A longer prompt can be cut into longer and fewer segments, so their number
+    // alone would have a small call need more than a large one. What is asked for
+    // is a bound that grows with B and n_tok: segments have two chunks or more, and
+    // (chunks + B) H / 512 or more, so fewer than 512 / H full ones are made.
+    const int64_t bound = std::min<int64_t>((n_tok - 1) / kLinChunk / 2, 512 / H);
+    more = std::max(bound, lin_split(B, n_tok, H).more);
+  }
+  // the states, then their decays
+  *bytes = lin_ws_state_bytes(more, H, dk, dv) + ((size_t)(2 * more) * H * sizeof(float) + 15) / 16 * 16;
   return KDA_OK;
 }
 
@@ -865,7 +875,7 @@ int kda_lin_prefill(float *cache, int64_t num_slots, int64_t slot_stride, const 
   a.seg = s.seg;
   a.more = (int32_t)s.more;
   a.ws = static_cast<float *>(workspace);
-  a.wdec = reinterpret_cast<float *>(static_cast<char *>(workspace) + lin_ws_state_bytes(s, H, dk, dv));
+  a.wdec = reinterpret_cast<float *>(static_cast<char *>(workspace) + lin_ws_state_bytes(s.more, H, dk, dv));
   if (n_tok == 0) a.group = 1;  // no tokens, no key heads
   // workgroups for (unit, head), the (unit, key head) pairs dealt to the 8 XCDs
   const auto blocks = [&](int64_t units) { return (units * (H / a.group) + 7) / 8 * 8 * a.group; };

@@ -700,8 +700,9 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
   if (ck == 0 && seg == 0) S.store(ckpt, false);
   if (r.n == 0) return;
 
-  const int first = seg * a.seg * kLinChunk;          // tokens of the row before the segment
-  const int n = min(r.n - first, a.seg * kLinChunk);  // and in it
+  const int64_t full = (int64_t)a.seg * kLinChunk;
+  const int first = (int)(seg * full);                    // tokens of the row before the segment
+  const int n = (int)min((int64_t)(r.n - first), full);  // and in it
   const int64_t tok0 = (int64_t)r.c0 + first;
   const uint16_t *q = a.q + tok0 * a.qs + (int64_t)(h / a.group) * DK;
   const uint16_t *k = a.k + tok0 * a.ks + (int64_t)(h / a.group) * DK;

@@ -41,7 +41,7 @@ def kda_lin_decode_step(cache: torch.Tensor, slot_ids: torch.Tensor, q, k, v, al
 
 
 def kda_lin_prefill_workspace(B: int, n_tok: int, H: int, dk: int, dv: int) -> int:
-    """Workspace bytes kda_lin_prefill needs for these sizes (0: none)."""
+    """Workspace bytes kda_lin_prefill needs for these sizes (0: none), never less for a larger B or n_tok."""
     n = ctypes.c_size_t(0)
     rc = load_library().kda_lin_prefill_workspace(B, n_tok, H, dk, dv, ctypes.byref(n))
     if rc != KDA_OK:

@@ -89,7 +89,9 @@ int kda_lin_prefill(float *cache, int64_t num_slots, int64_t slot_stride, const 
                     void *workspace, size_t workspace_bytes, int32_t *dev_err, const kda_options *opts,
                     void *stream);
 
-/* Host only. Workspace bytes kda_lin_prefill needs for these sizes (to *bytes). */
+/* Host only. Workspace bytes kda_lin_prefill needs for these sizes (to *bytes): never less for a larger B or
+ * n_tok, so that a buffer for the largest call serves the smaller ones, and at most 1024 states of dk x dv with a
+ * decay each (64 MiB and 4 KiB at 128 x 128). */
 int kda_lin_prefill_workspace(int32_t B, int32_t n_tok, int32_t H, int32_t dk, int32_t dv, size_t *bytes);
 
 #ifdef __cplusplus

@@ -1,4 +1,5 @@
-"""Workspaces of the prefill calls on the GPU: the stream they are allocated on."""
+"""Workspaces of the prefill calls on the GPU: the stream they are allocated on, and one kept for
+calls of several sizes."""
 
 import numpy as np
 import pytest
@@ -77,3 +78,22 @@ def test_chunk_prefill_workspace_comes_from_the_stream_of_the_launch():
         torch.cuda.synchronize()
         assert {s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] not in before} == {handle}
     torch.cuda.empty_cache()
+
+
+def test_one_workspace_for_calls_of_several_sizes():
+    """A buffer for the largest call, full of NaN, serves the smaller ones in turn; the bits are those of the calls alone."""
+    H, d = 32, 128
+    sizes = [8000, 4096, 3840, 2560, 700]
+    ws = torch.full((K.kda_lin_prefill_workspace(1, max(sizes), H, d, d),), 0xFF, dtype=torch.uint8, device=dev())
+    p = inputs(191, max(sizes), H, 4, d, d, True)
+    q, k, v = split(p, p["x"].to(dev()))
+    al, cache0 = p["alpha"].to(dev()), cache_of(3, 1, H, d, d).to(dev())
+    for n in sizes:
+        log(f"lin prefill of {n} tokens with the workspace of the largest call")
+        got = []
+        for w in (None, ws):
+            cache, out = cache0.clone(), torch.empty(n, H, d, device=dev())
+            K.kda_lin_prefill(cache, i32([0]), i32([0, n]), q[:n], k[:n], v[:n], al[:n], out, workspace=w)
+            torch.cuda.synchronize()
+            got.append((bits(cache), bits(out)))
+        assert all(np.array_equal(x, y) for x, y in zip(*got)), n
