@@ -12,6 +12,7 @@
 
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -213,6 +214,8 @@ PyObject *guarded(F &&f) {
     PyErr_SetString(PyExc_TypeError, e.what());
   } catch (const ValueError &e) {
     PyErr_SetString(PyExc_ValueError, e.what());
+  } catch (const c10::Error &) {  // as torch raises it: OutOfMemoryError for a workspace that does not fit
+    torch::translate_exception_to_python(std::current_exception());
   } catch (const std::exception &e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {

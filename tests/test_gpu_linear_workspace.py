@@ -97,3 +97,27 @@ def test_one_workspace_for_calls_of_several_sizes():
             torch.cuda.synchronize()
             got.append((bits(cache), bits(out)))
         assert all(np.array_equal(x, y) for x, y in zip(*got)), n
+
+
+@pytest.mark.parametrize("kind", ["current", "handle 0", "side stream"])
+def test_a_workspace_that_does_not_fit_is_torchs_out_of_memory_error(kind):
+    """What a server catches around kda_prefill_chunked. The allocator is limited to what it holds already, so that
+    the call's workspace is refused on the host; afterwards the same call runs."""
+    args, _ = long_prompt(201)
+    stream = {"current": None, "handle 0": 0, "side stream": torch.cuda.Stream()}[kind]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    before = bits(args[0])
+    total = torch.cuda.get_device_properties(0).total_memory
+    log(f"lin prefill without room for its workspace, stream {kind}")
+    torch.cuda.set_per_process_memory_fraction(torch.cuda.memory_reserved() / total)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            K.kda_lin_prefill(*args, stream=stream)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    torch.cuda.synchronize()
+    assert np.array_equal(bits(args[0]), before)
+    K.kda_lin_prefill(*args, stream=stream)
+    torch.cuda.synchronize()
+    assert not np.array_equal(bits(args[0]), before)
