@@ -141,10 +141,10 @@ kda_lin_tokens tokens(const Cache &c, int64_t rows, PyObject *q, PyObject *k, Py
   const Strided qs = heads(q, "q", c.dev, rows, Hk, c.dk), ks = heads(k, "k", c.dev, rows, Hk, c.dk),
                 vs = heads(v, "v", c.dev, rows, c.H, c.dv);
   const bool fixed = tensor(alpha, "alpha").dim() == 1;
-  const void *a = fixed ? contiguous(alpha, "alpha", c.dev, is_f32, kF32, {c.H})
-                        : contiguous(alpha, "alpha", c.dev, is_f32, kF32, {rows, c.H});
+  const Strided as = fixed ? Strided{contiguous(alpha, "alpha", c.dev, is_f32, kF32, {c.H}), 0}
+                           : rows_of(alpha, "alpha", c.dev, is_f32, kF32, rows, c.H);
   return {static_cast<const uint16_t *>(qs.p), static_cast<const uint16_t *>(ks.p), static_cast<const uint16_t *>(vs.p),
-          static_cast<const float *>(a), qs.stride, ks.stride, vs.stride, fixed ? 0 : c.H, i32(Hk)};
+          static_cast<const float *>(as.p), qs.stride, ks.stride, vs.stride, as.stride, i32(Hk)};
 }
 
 int32_t *dev_err_of(PyObject *o, int dev) {

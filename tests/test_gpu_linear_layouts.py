@@ -1,0 +1,54 @@
+"""Layouts of the linear-attention calls' arguments: what is taken, what is refused."""
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_98_amd as K
+from gpu_util import bits, dev, i32, log
+from test_gpu_linear import cache_of, inputs, split
+
+pytestmark = pytest.mark.gpu
+
+H, D = 4, 64
+
+
+def call(op, p, alpha, out=None, n=70):
+    """(cache, out) of one call on its own copies."""
+    q, k, v = split(p, p["x"].to(dev()))
+    cache = cache_of(5, n if op == "decode" else 2, H, D, D).to(dev())
+    out = torch.empty(n, H, D, device=dev()) if out is None else out
+    if op == "decode":
+        K.kda_lin_decode_step(cache, i32(np.arange(n)), q, k, v, alpha, out)
+    else:
+        K.kda_lin_prefill(cache, i32([1, 0]), i32([0, 40, n]), q, k, v, alpha, out)
+    torch.cuda.synchronize()
+    return bits(cache), bits(out)
+
+
+@pytest.mark.parametrize("op", ["decode", "prefill"])
+def test_decays_with_a_stride_between_tokens(op):
+    """alpha as a slice of a wider projection, and as one row of decays expanded over the tokens."""
+    p = inputs(211, 70, H, 2, D, D, True)
+    ref = call(op, p, p["alpha"].to(dev()))
+    wide = torch.full((70, 2 * H + 3), float("nan"), device=dev())
+    wide[:, 3: 3 + H] = p["alpha"].to(dev())
+    log(f"lin {op}: decays sliced out of rows of {2 * H + 3}")
+    got = call(op, p, wide[:, 3: 3 + H])
+    assert all(np.array_equal(x, y) for x, y in zip(got, ref))
+    fixed = p["alpha"][7].to(dev())
+    log(f"lin {op}: expanded decays")
+    got = call(op, p, fixed.expand(70, H))
+    assert all(np.array_equal(x, y) for x, y in zip(got, call(op, p, fixed)))
+
+
+@pytest.mark.parametrize("op", ["decode", "prefill"])
+def test_decays_refused(op):
+    p = inputs(212, 70, H, 2, D, D, True)
+    al = p["alpha"].to(dev())
+    for bad in (al.t().contiguous().t(), al.repeat_interleave(2, 1)[:, ::2], al[0].repeat_interleave(2)[::2], al[:, :1].expand(70, H)):
+        with pytest.raises(ValueError):
+            call(op, p, bad)
+    with pytest.raises(K.KdaError) as e:  # overlapping rows
+        call(op, p, al.flatten().as_strided((70, H), (1, 1)))
+    assert e.value.status == K.KDA_ERR_INVALID
