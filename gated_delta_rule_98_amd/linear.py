@@ -32,8 +32,8 @@ def kda_lin_decode_step(cache: torch.Tensor, slot_ids: torch.Tensor, q, k, v, al
 
     cache float32 [num_slots, H, dv, dk]; slot_ids int32 [B]; q, k bf16 [B, Hk, dk] with Hk dividing
     H; v bf16 [B, H, dv]; alpha float32 [H] (fixed) or [B, H] (q, k, v and alpha may be slices with any
-    stride between tokens); out float32 or bf16 [B, H, dv]; gate bf16 [B, H, dv] (optional output gate),
-    weight float32 [dv].
+    stride between tokens); out float32 or bf16 [B, H, dv], 16-byte aligned (bf16: 8); gate bf16
+    [B, H, dv] (optional output gate), 8-byte aligned; weight float32 [dv].
     """
     rc = native().lin_decode_step(cache, slot_ids, q, k, v, alpha, out, gate, weight, eps, dev_err, tile_w, stream)
     if rc != KDA_OK:

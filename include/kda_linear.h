@@ -16,7 +16,8 @@
  *   v       bf16   token t's heads at v + t * v_stride, laid out [H][dv]
  *   alpha   float  token t's decays at alpha + t * alpha_stride, laid out [H];
  *                  alpha_stride = 0: the same decays for every token
- *   out     float  [rows][H][dv], contiguous (bf16 with KDA_OUT_BF16)
+ *   out     float  [rows][H][dv], contiguous, 16-byte aligned (with KDA_OUT_BF16
+ *                  bf16, 8-byte aligned): stricter than kda.h's, KDA_ERR_ALIGN
  * Hk divides H: heads h of H / Hk consecutive ones share key head h / (H / Hk).
  * q is used as given: any 1/sqrt(dk) scale is the caller's.
  *
@@ -61,7 +62,7 @@ typedef struct kda_lin_tokens {
 /*
  * Single-token step for B rows: row b reads token b, updates the state of slot
  * slot_ids[b] in place (all H heads) and writes out[b]. With epi the output
- * gate of kda.h is applied (gate bf16 [B][H][dv], contiguous). Slot ids must be
+ * gate of kda.h is applied (gate bf16 [B][H][dv], contiguous, 8-byte aligned). Slot ids must be
  * distinct. tile_w: 0 or one of 4, 8, 16, 32, 64, 128 with tile_w <= dv (and
  * tile_w == dv with the gate); results are bit-identical for every width.
  */

@@ -52,3 +52,25 @@ def test_decays_refused(op):
     with pytest.raises(K.KdaError) as e:  # overlapping rows
         call(op, p, al.flatten().as_strided((70, H), (1, 1)))
     assert e.value.status == K.KDA_ERR_INVALID
+
+
+@pytest.mark.parametrize("op", ["decode", "prefill"])
+@pytest.mark.parametrize("dtype,step", [(torch.float32, 4), (torch.bfloat16, 4)], ids=["fp32", "bf16"])
+def test_alignment_of_outputs(op, dtype, step):
+    """out may start 16 bytes (bf16: 8) into an allocation, and nowhere in between."""
+    p = inputs(213, 70, H, 2, D, D, True)
+    al = p["alpha"].to(dev())
+    ref = call(op, p, al, torch.empty(70, H, D, dtype=dtype, device=dev()))
+    buf = torch.zeros(70 * H * D + 8, dtype=dtype, device=dev())
+    for off in range(1, 9):
+        out = buf[off: off + 70 * H * D].view(70, H, D)
+        log(f"lin {op}: out {off} elements of {dtype} into its allocation")
+        if off % step:
+            with pytest.raises(K.KdaError) as e:
+                call(op, p, al, out)
+            assert e.value.status == K.KDA_ERR_ALIGN
+        else:
+            buf.zero_()
+            got = call(op, p, al, out)
+            assert all(np.array_equal(x, y) for x, y in zip(got, ref))
+            assert not buf[:off].any() and not buf[off + 70 * H * D:].any()
