@@ -10,9 +10,11 @@
  * gate the sigmoid is 1, without z r' = r (the first norm of a model), without
  * y only r' is written (the last block). Every intermediate is fp32; y is the
  * norm of the fp32 sum r', also where resid_out rounds it to bf16. The gate is
- * read and applied as kda_epilogue's is. Squares are fp32 too: a row with values
- * past about 1e19 overflows its mean square and N is 0 there, or NaN with an
- * infinity; with eps = 0 a row of zeros gives NaN.
+ * read and applied as kda_epilogue's is. A row's sum of squares is fp32 too: past
+ * 3.4e38 (D values of 1.8e19 / sqrt(D)) N is 0 in the row, or NaN with an infinity.
+ * Squares below 1.2e-38 (values below 1.1e-19) lose bits and below 1e-45 are 0,
+ * which shows only where eps is no larger: with eps = 0 a row of such values gives
+ * infinities and one of zeros NaN.
  */
 #ifndef KDA_NORM_H
 #define KDA_NORM_H

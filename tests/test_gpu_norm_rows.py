@@ -1,5 +1,5 @@
 """Block norms of more rows than workgroups are launched: a workgroup walks several rows, requesting the next one
-while it sums and stores this one."""
+while it sums and stores this one. And rows at the ends of the range in which squares are fp32."""
 
 import numpy as np
 import pytest
@@ -45,3 +45,20 @@ def test_a_row_does_not_depend_on_where_it_stands(rows, D):
                 pad=pad)
         for x, y in zip(a, b):
             assert np.array_equal(bits(x.contiguous())[order.numpy()], bits(y.contiguous()))
+
+
+@pytest.mark.parametrize("D", [64, 2051, 16384])
+def test_ends_of_the_range_of_squares(D):
+    """Without eps: rows of values from 2^-60 to 2^63 / sqrt(D) are normalized as any others; a row whose squares sum
+    past fp32's range gives 0, one whose squares are all 0 infinities, one of zeros NaN."""
+    c = make(D, 7, D, (0, 0, 0, 1), False)
+    unit = c["resid"].sign() * (1 + torch.rand(7, D, generator=torch.Generator().manual_seed(1)))
+    unit[unit == 0] = 1.0
+    scale = torch.tensor([2.0 ** -60, 2.0 ** -30, 1.0, 2.0 ** 62 / D ** 0.5, 2.0 ** 64, 2.0 ** -80, 0.0])
+    c["resid"] = unit * scale[:, None]
+    log(f"norm of rows of 2^-80 to 2^64, D={D}, eps 0")
+    _, y = run(c, False, eps=0.0)
+    check(dict(c, resid=c["resid"][:4]), (None, y[:4]), False, eps=0.0)
+    assert not y[4].any()
+    assert torch.isinf(y[5]).all()
+    assert torch.isnan(y[6]).all()
