@@ -25,8 +25,6 @@ CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("kda_api.hip", "kda_decode.hip", "kda_verify.hip",
                                            "kda_verify_chunk.hip", "kda_prefill.hip", "kda_prefill_chunk.hip",
                                            "kda_state.hip", "kda_linear.hip", "kda_norm.hip")]
-HEADERS = [os.path.join(CSRC, "kda_engine.h"), os.path.join(ROOT, "include", "kda.h"),
-           os.path.join(ROOT, "include", "kda_linear.h"), os.path.join(ROOT, "include", "kda_norm.h")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkda.so")
 # the benchmark's ceiling probes (csrc/probe/): not part of the KDA library or its C ABI

@@ -928,7 +928,6 @@ int kda_block_norm(const void *resid, int64_t resid_stride, const uint16_t *z, i
   a.eps = eps;
   a.rows = rows;
   a.D = D;
-  a.resid_bf16 = rb == 2;
   a.y_bf16 = yb == 2;
   const NormLaunch l = norm_launch(rows, D, rb == 2);
   void *args[] = {&a};

@@ -60,7 +60,7 @@ struct NormArgs {
   const float *w_post, *w_pre;
   int64_t rs, zs, ros, ys, gs;
   float scale, eps;
-  int32_t rows, D, resid_bf16, y_bf16;
+  int32_t rows, D, y_bf16;
 };
 
 // Kernel, threads and workgroups of a block norm.
