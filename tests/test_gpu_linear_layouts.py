@@ -74,3 +74,65 @@ def test_alignment_of_outputs(op, dtype, step):
             got = call(op, p, al, out)
             assert all(np.array_equal(x, y) for x, y in zip(got, ref))
             assert not buf[:off].any() and not buf[off + 70 * H * D:].any()
+
+
+def test_calls_of_nothing():
+    """No rows, no tokens: nothing is written and nothing fails."""
+    none = torch.zeros(0, H, D, dtype=torch.bfloat16, device=dev())
+    cache = cache_of(5, 2, H, D, D).to(dev())
+    before = bits(cache)
+    al, out = torch.ones(H, device=dev()), torch.empty(0, H, D, device=dev())
+    log("lin decode, prefill and norm of nothing")
+    K.kda_lin_decode_step(cache, i32([]), none, none, none, al, out)
+    K.kda_lin_decode_step(cache, i32([]), none, none, none, al.expand(0, H), out, gate=none)
+    K.kda_lin_prefill(cache, i32([]), i32([0]), none, none, none, al, out)
+    K.kda_lin_prefill(cache, i32([1, 0]), i32([0, 0, 0]), none, none, none, al.expand(0, H), out)
+    K.kda_block_norm(torch.zeros(0, 64, device=dev()), y=torch.zeros(0, 64, device=dev()), w_pre=torch.ones(64, device=dev()))
+    torch.cuda.synchronize()
+    assert np.array_equal(bits(cache), before)
+
+
+@pytest.mark.parametrize("op", ["decode", "prefill"])
+def test_bfloat16_bits_as_integers(op):
+    p = inputs(214, 70, H, 2, D, D, True)
+    al = p["alpha"].to(dev())
+    ref = call(op, p, al, torch.empty(70, H, D, dtype=torch.bfloat16, device=dev()))
+    log(f"lin {op}: bits as int16")
+    got = call(op, dict(p, x=p["x"].view(torch.int16)), al, torch.empty(70, H, D, dtype=torch.int16, device=dev()))
+    assert np.array_equal(got[0], ref[0]) and np.array_equal(got[1], ref[1])
+
+
+@pytest.mark.parametrize("n,heads", [(2000, 8), (70, 4)], ids=["segments", "short"])
+def test_captured_with_the_stream_named(n, heads):
+    """A prompt and a step captured with stream= the captured stream, its workspace allocated under the capture; every
+    replay against the eager run, with eager work between."""
+    p = inputs(215, n, heads, 2, D, D, True)
+    q, k, v = split(p, p["x"].to(dev()))
+    cache0 = cache_of(5, 1, heads, D, D).to(dev())
+    cache, out = cache0.clone(), torch.empty(n, heads, D, device=dev())
+    s, cu, al = i32([0]), i32([0, n]), p["alpha"].to(dev())
+
+    def work(stream):
+        K.kda_lin_prefill(cache, s, cu, q, k, v, al, out, stream=stream)
+        K.kda_lin_decode_step(cache, s, q[:1], k[:1], v[:1], al[:1], out[:1], stream=stream)
+
+    work(None)
+    torch.cuda.synchronize()
+    ref = bits(cache), bits(out)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    log(f"lin capture with the stream named, {n} tokens")
+    with torch.cuda.graph(graph, stream=side):
+        work(side)
+    for r in range(3):
+        cache.copy_(cache0)
+        out.zero_()
+        torch.cuda.synchronize()
+        log(f"replay {r}")
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(bits(cache), ref[0]) and np.array_equal(bits(out), ref[1]), r
+        cache.copy_(cache0)
+        work(0)
+        torch.cuda.synchronize()
+        assert np.array_equal(bits(cache), ref[0]) and np.array_equal(bits(out), ref[1]), r
