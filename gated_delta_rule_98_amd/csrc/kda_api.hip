@@ -769,23 +769,24 @@ int kda_lin_decode_step(float *cache, int64_t num_slots, int64_t slot_stride, co
 // Prefill takes one workgroup per (row, head, 16 value columns) that walks the
 // row (lin_walk_kernel) for short prompts of few heads, else one per (segment,
 // head). Measured on MI355X, us, walking / in segments: one row of 32 heads,
-// 128 x 128: 37 tokens 6.8 / 11.3, 256 tokens 14.4 / 26, 512 24.6 / 31, 768
-// 34.4 / 34, 1024 43.5 / 38; 64 x 64: 512 tokens 15.5 / 19, 1024 28.7 / 23.5.
-// 512 workgroups: 8 rows x 8 heads of 512 tokens 19.0 / 26.6, 2 x 32 of 256
-// 17.8 / 17.0; 1024 workgroups: 4 x 32 of 256 23.7 / 12.8.
+// 128 x 128: 37 tokens 6.8 / 11.1, 256 tokens 14.0 / 27.5, 512 24 / 30, 768
+// 33.6 / 33.2, 1024 42 / 37; 64 x 64: 512 tokens 15.2 / 19.4, 1024 28 / 23.5.
+// 512 workgroups: 8 ragged rows x 8 heads of 512 tokens in all 18.6 / 30, 2 x 32 of
+// 256 in all 17.8 / 16.8; 1024 workgroups: 4 x 32 of 256 in all 23.4 / 12.7.
 static bool lin_walks(int32_t B, int32_t n_tok, int32_t H, int32_t dv) {
   return (int64_t)B * H * lin_walk_tiles(dv) <= 512 && n_tok <= 640;
 }
 
 // Chunks per segment and the segments past the rows' first ones. Many chunks are
 // shared by about 512 (segment, head) workgroups, two per CU: cutting further
-// moves more states, cutting less leaves CUs idle (8000 tokens x 32 heads, us, at
-// 256, 512 and 1024 workgroups: 167, 153, 168). Few are cut to about 256, but to
+// moves more states, cutting less leaves CUs idle (us at 256, 512 and 1024
+// workgroups: 8000 tokens x 32 heads of 128 x 128 153, 150, 165; 2 rows of 16384 x 32
+// of 64 x 64 265, 224, 237; 16 ragged rows of 5003 in all 129, 107, 115). Few are cut to about 256, but to
 // no less than 2 and no more than 4 chunks each, where a chunk's latency counts
 // against that of chaining the segments (1024 tokens x 32 heads, 2 and 4 chunks:
-// 38, 44; 2048 x 32: 60, 53; 2048 x 8: 33, 42; 8000 x 8: 70, 60); with rows of
+// 37, 43; 2048 x 32: 59, 51; 2048 x 8: 32, 41; 8000 x 8: 67, 56); with rows of
 // under 4 chunks on average not below 4, since rows that need no cut would still
-// pay for three launches (4 rows of 64 tokens x 32 heads: 18, 12.8). Rows of at
+// pay for three launches (4 rows of 64 tokens x 32 heads: 18, 12.7). Rows of at
 // most that many chunks are one segment. A row of n tokens has at most
 // (n - 1) / 64 chunks after its first, so the rows together have at most
 // (n_tok - 1) / 64 / seg segments after their first ones.

@@ -561,8 +561,8 @@ __device__ __forceinline__ void tile_decay(const ChunkDecay &d, int st, int tt, 
 // ---- the state sum of every segment that another one follows ----
 //
 // Reads k and v once; a wave has 16 columns of the state over all key channels
-// in accumulators. 8000 tokens x 32 heads of 128 x 128: 44 us for 126 MB read and
-// 31 written (3.6 TB/s); two rows of 16384 x 32 of 64 x 64: 66 us for 242 and 7.
+// in accumulators. 8000 tokens x 32 heads of 128 x 128: 43.5 us for 126 MB read and
+// 31 written (3.6 TB/s); two rows of 16384 x 32 of 64 x 64: 64 us for 242 and 7.
 template <int DK, int DV>
 __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_sum_kernel(LinArgs a) {
   constexpr int NT = lin_threads(DV), NW = NT / 64;
@@ -625,7 +625,7 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_sum_kernel(L
 //
 // A thread takes 4 elements through the row's segments. One row of 15 full
 // segments x 32 heads of 128 x 128: 13 us, a chain of loads from the Infinity
-// Cache; 16 ragged rows of 5003 tokens in all 13 us (a workgroup for every row and
+// Cache; 16 ragged rows of 5003 tokens in all 12.5 us (a workgroup for every row and
 // head, most of them of rows that are not cut).
 template <int DK, int DV>
 __global__ __launch_bounds__(lin_threads(DV)) void lin_scan_kernel(LinArgs a) {
@@ -651,15 +651,17 @@ __global__ __launch_bounds__(lin_threads(DV)) void lin_scan_kernel(LinArgs a) {
 
 // ---- outputs, final state and checkpoint ----
 //
-// 8000 tokens x 32 heads of 128 x 128, fp32 out: 90 to 105 us with the clock (84
-// where it is 100 if every chunk's inputs are resident in L2), so what bounds it is
-// mostly not HBM. A chunk of one head takes a wave 48 MFMAs for S0^T q, 5 for the
+// 8000 tokens x 32 heads of 128 x 128, fp32 out: 88 us once the clock has settled (98
+// to 115 in a process's first calls; with every chunk's inputs resident in L2 a sixth
+// less), so what bounds it is mostly not HBM. A chunk of one head takes a wave 48 MFMAs for S0^T q, 5 for the
 // scores, 18 for their product with v and 48 for the state, and as many cycles of
-// VALU work to split the fp32 operands, in phases that barriers keep apart: MFMA
-// and VALU are busy about a third of the time each. 8 waves of 16 columns keep 128
-// registers and so two workgroups per CU; 4 waves of 32 columns spilled (137 us).
-// Bank conflicts count little: with the transposing reads' two rows apart, which
-// takes a fifth of them away, the times were the same within 1%.
+// VALU work to split the fp32 operands, in phases that barriers keep apart. Every
+// wave reads all of q, k and the scores from LDS, 0.5 MB a chunk: the LDS is busy
+// 56% of the time (25% in bank conflicts), VALU 40%, MFMA 36%. 8 waves of 16 columns
+// keep 128 registers and so two workgroups per CU. 4 waves of 32 columns, which would
+// halve those reads, spilled hoisted addresses when they were tried (137 us); they
+// have not been timed with the addresses pinned. The transposing reads' two rows
+// apart, which takes a fifth of the conflicts away: the same within 1%.
 template <int DK, int DV, bool BF16>
 __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(LinArgs a) {
   constexpr int NT = lin_threads(DV), NW = NT / 64, KB = DK / 32, T = kLinChunk / kLB;
@@ -671,9 +673,9 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
   int unit, h;
   LinRow r;
   // Every row's last segment, then the full ones (measured on MI355X, the whole
-  // prefill of 32 heads, us, and the other way round: 2 rows of 16384 tokens x
-  // 64 x 64 206, 230; 16 ragged rows of 5003 tokens in all 98, 102; 32 of 8000
-  // 158, 173; 8 of 8000 139, 134).
+  // prefill of 32 heads, bfloat16 out, us, and the other way round: 2 rows of 16384
+  // tokens x 64 x 64 221, 239; 16 ragged rows of 5003 tokens in all 104, 111; 32 of
+  // 8000 170, 184; 8 of 8000 149, 142, of 1000 each 134, 128).
   if (!lin_unit_head(a, a.more + a.B, unit, h)) return;
   int seg;
   if (unit >= a.B) {
@@ -842,7 +844,7 @@ __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(L
 // LDS one ahead. Every column tile forms the scores again, so this costs more
 // work in total than the kernel above (8000 tokens x 32 heads: 337 us); lin_walks
 // (kda_api.hip) says where it wins. 37 tokens x 32 heads of 128 x 128: 7.0 us
-// (the kernel above 11.3), a chunk more takes 2.5 us.
+// (the kernel above 11.1), a chunk more takes 2.5 us.
 
 constexpr int kWalkTile = 16, kWalkOutWaves = 6;
 

@@ -30,8 +30,9 @@ struct LinArgs {
 
 // Slabs of columns per lane of the gated single-token step, whose workgroup owns
 // all dv columns of a head (waves = dv / (4 * slabs)). Measured on MI355X at 2, 4
-// and 8 slabs: 13 rows x 24 heads at 64 x 128 8.3, 7.7, 7.2 us; 8 x 32 at
-// 128 x 128 9.5, 8.8, 8.5; 64 x 32 46.8, 49.3, 47.7.
+// and 8 slabs: 13 rows x 24 heads at 64 x 128 8.3, 7.7, 7.2 us (the last 6.6 in a
+// later run); 8 x 32 at 128 x 128 9.5, 8.8, 8.5; 64 x 32 46.8, 49.3, 47.7: 8 wins
+// where latency counts and gives up 2% of the largest batch.
 constexpr int kLinGateSlabs = 8;
 const void *lin_decode_kernel_for(int dk, int C, bool gate, bool bf16);
 

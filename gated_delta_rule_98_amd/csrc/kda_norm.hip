@@ -219,9 +219,9 @@ const void *norm_of(bool rb, bool tail) {
 }  // namespace
 
 // Measured on MI355X at D = 4096. Up to 512 rows (two per CU) latency counts and
-// a row takes 512 threads: 64 rows with every part 4.6 us, 5.1 with 256. Past
+// a row takes 512 threads: 64 rows with every part 4.5 us, 4.9 with 256. Past
 // that a row takes 256 and a workgroup several rows, 4096 workgroups at most:
-// 8000 rows with every part 59.4 us (5.5 TB/s), 60.4 with 512 threads, 69 with a
+// 8000 rows with every part 59.7 us (5.5 TB/s), 60.4 with 512 threads, 69 with a
 // row per workgroup, its weights read for every row and no streaming hints.
 constexpr int kFewRows = 512, kMostBlocks = 4096;
 
