@@ -1,6 +1,8 @@
 """Workspaces of the prefill calls on the GPU: the stream they are allocated on, and one kept for
 calls of several sizes."""
 
+import contextlib
+
 import numpy as np
 import pytest
 import torch
@@ -22,6 +24,18 @@ def long_prompt(seed, n=4000, H=32):
     return args, need
 
 
+def streams_of_allocations(call, size):
+    """The streams' handles of the allocations of at least `size` bytes that torch makes during the call."""
+    torch.cuda.memory._record_memory_history(max_entries=1000, stacks="python")
+    try:
+        call()
+        torch.cuda.synchronize()
+        trace = torch.cuda.memory._snapshot()["device_traces"][0]
+    finally:
+        torch.cuda.memory._record_memory_history(enabled=None)
+    return [e["stream"] for e in trace if e["action"] == "alloc" and e["size"] >= size]
+
+
 @pytest.mark.parametrize("kind", ["none", "handle 0", "default stream", "current stream", "side stream", "side handle"])
 def test_workspace_comes_from_the_stream_of_the_launch(kind):
     args, need = long_prompt(171)
@@ -31,15 +45,8 @@ def test_workspace_comes_from_the_stream_of_the_launch(kind):
                       "current stream": (torch.cuda.current_stream(), 0), "side stream": (side, side.cuda_stream),
                       "side handle": (side.cuda_stream, side.cuda_stream)}[kind]
     torch.cuda.synchronize()
-    torch.cuda.empty_cache()
-    before = {s["address"] for s in torch.cuda.memory_snapshot()}
     log(f"lin prefill on stream {kind}")
-    K.kda_lin_prefill(*args, stream=stream)
-    torch.cuda.synchronize()
-    new = [s for s in torch.cuda.memory_snapshot() if s["address"] not in before]
-    assert sum(s["total_size"] for s in new) >= need
-    assert {s["stream"] for s in new} == {handle}
-    torch.cuda.empty_cache()
+    assert streams_of_allocations(lambda: K.kda_lin_prefill(*args, stream=stream), need) == [handle]
 
 
 def test_calls_on_the_default_stream_and_on_pool_streams_at_once():
@@ -64,20 +71,15 @@ def test_calls_on_the_default_stream_and_on_pool_streams_at_once():
 
 def test_chunk_prefill_workspace_comes_from_the_stream_of_the_launch():
     n, H, d = 2000, 32, 128
-    assert K.kda_prefill_chunked_workspace(1, n, H, d, d) >= 32 << 20
+    need = K.kda_prefill_chunked_workspace(1, n, H, d, d)
     x = torch.full((n, H, d), 0.05, dtype=torch.bfloat16, device=dev())
     args = (torch.zeros(1, H, d, d, device=dev()), i32([0]), i32([0, n]), x, x, x, torch.full((n, H, d), 0.9, device=dev()),
             torch.full((n, H), 0.5, device=dev()), torch.empty(n, H, d, device=dev()))
     side = torch.cuda.Stream()
-    for stream, handle in ((0, 0), (side, side.cuda_stream)):
+    for stream, handle in ((0, 0), (side, side.cuda_stream), (None, 0)):
         torch.cuda.synchronize()
-        torch.cuda.empty_cache()
-        before = {s["address"] for s in torch.cuda.memory_snapshot()}
         log(f"chunk prefill on stream handle {'0' if handle == 0 else 'of a side stream'}")
-        K.kda_prefill_chunked(*args, stream=stream)
-        torch.cuda.synchronize()
-        assert {s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] not in before} == {handle}
-    torch.cuda.empty_cache()
+        assert streams_of_allocations(lambda: K.kda_prefill_chunked(*args, stream=stream), need) == [handle]
 
 
 def test_one_workspace_for_calls_of_several_sizes():
@@ -101,9 +103,10 @@ def test_one_workspace_for_calls_of_several_sizes():
 
 @pytest.mark.parametrize("kind", ["current", "handle 0", "side stream"])
 def test_a_workspace_that_does_not_fit_is_torchs_out_of_memory_error(kind):
-    """What a server catches around kda_prefill_chunked. The allocator is limited to what it holds already, so that
-    the call's workspace is refused on the host; afterwards the same call runs."""
-    args, _ = long_prompt(201)
+    """What a server catches around kda_prefill_chunked. The allocator is limited to what it holds already and every
+    block of it that would do is taken, so that the call's workspace is refused on the host; afterwards the same call
+    runs."""
+    args, need = long_prompt(201)
     stream = {"current": None, "handle 0": 0, "side stream": torch.cuda.Stream()}[kind]
     torch.cuda.synchronize()
     torch.cuda.empty_cache()
@@ -111,10 +114,16 @@ def test_a_workspace_that_does_not_fit_is_torchs_out_of_memory_error(kind):
     total = torch.cuda.get_device_properties(0).total_memory
     log(f"lin prefill without room for its workspace, stream {kind}")
     torch.cuda.set_per_process_memory_fraction(torch.cuda.memory_reserved() / total)
+    taken = []
     try:
+        with torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext():
+            with contextlib.suppress(torch.OutOfMemoryError):
+                for _ in range(torch.cuda.memory_reserved() // need + 1):
+                    taken.append(torch.empty(need, dtype=torch.uint8, device=dev()))
         with pytest.raises(torch.OutOfMemoryError):
             K.kda_lin_prefill(*args, stream=stream)
     finally:
+        del taken
         torch.cuda.set_per_process_memory_fraction(1.0)
     torch.cuda.synchronize()
     assert np.array_equal(bits(args[0]), before)
