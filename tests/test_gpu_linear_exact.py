@@ -118,3 +118,29 @@ def test_decays_reach_scores_and_states_with_all_their_bits(lens, H, Hk, dk, dv,
         assert err == 0
         assert torch.equal(out[:n], want.bfloat16() if bf16 else want)
         assert torch.equal(cache, state)
+
+
+@pytest.mark.parametrize("H", [2, 80])
+def test_small_values(H):
+    """bfloat16 inputs below fp32's normal range are not flushed; states are read to 2^-133, the smallest bfloat16, and
+    kept as they are."""
+    n, d = 70, 128
+    p = inputs(261, n, H, H, d, d, False, decay="ones")
+    q = torch.zeros(n, H, d)
+    e = torch.arange(n) % 10 - 133
+    q[torch.arange(n), :, 5] = torch.exp2(e.double()).float()[:, None]
+    log(f"lin prefill with q down to 2^-133, H={H}")
+    out, cache, _, _ = run_prefill(prompt(p, n, k=torch.zeros(n, H, d), q=q), [n], np.array([0], np.int32),
+                                   torch.full((1, H, d, d), 2.0 ** 100))
+    assert torch.equal(out, torch.exp2(e + 100.0)[:, None, None].expand(n, H, d)) and bool((cache == 2.0 ** 100).all())
+    g = torch.Generator().manual_seed(3)
+    S = ((1 + torch.rand(1, H, d, d, generator=g)).double() * torch.exp2(-100.0 - torch.randint(40, (1, H, d, d), generator=g))).float()
+    pick = torch.arange(n) % d
+    q = one_hot(pick[:, None].expand(n, H), d)
+    log(f"lin prefill with states down to 2^-139, H={H}")
+    out, cache, _, _ = run_prefill(prompt(p, n, k=torch.zeros(n, H, d), q=q), [n], np.array([0], np.int32), S)
+    want = S[0, :, :, pick].permute(2, 0, 1)
+    assert torch.equal(cache, S)
+    assert float((out.double() - want.double()).abs().max()) < 2.0 ** -133
+    big = want >= 2.0 ** -109
+    assert torch.equal(out[big], want[big])

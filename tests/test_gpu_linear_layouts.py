@@ -136,3 +136,21 @@ def test_captured_with_the_stream_named(n, heads):
         work(0)
         torch.cuda.synchronize()
         assert np.array_equal(bits(cache), ref[0]) and np.array_equal(bits(out), ref[1]), r
+
+
+@pytest.mark.parametrize("heads", [4, 72])
+def test_tokens_before_the_first_row(heads):
+    """cu_seqlens need not start at 0: the tokens before the first row are no row's, and their outputs stay."""
+    n, lead = 210, 7
+    p = inputs(216, n, heads, 2, D, D, True)
+    q, k, v = split(p, p["x"].to(dev()))
+    al, cache0 = p["alpha"].to(dev()), cache_of(5, 2, heads, D, D).to(dev())
+    ref, rout = cache0.clone(), torch.empty(n - lead, heads, D, device=dev())
+    log(f"lin prefill of rows that start at token {lead}, {heads} heads")
+    K.kda_lin_prefill(ref, i32([1, 0]), i32([0, 150, n - lead]), q[lead:].contiguous(), k[lead:].contiguous(), v[lead:].contiguous(),
+                      al[lead:].contiguous(), rout)
+    cache, out = cache0.clone(), torch.full((n, heads, D), 7.0, device=dev())
+    K.kda_lin_prefill(cache, i32([1, 0]), i32([lead, lead + 150, n]), q, k, v, al, out)
+    torch.cuda.synchronize()
+    assert np.array_equal(bits(cache), bits(ref)) and np.array_equal(bits(out[lead:]), bits(rout))
+    assert bool((out[:lead] == 7.0).all())
