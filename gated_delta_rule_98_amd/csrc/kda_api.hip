@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "kda_chunk.h"
@@ -898,7 +899,7 @@ int kda_block_norm(const void *resid, int64_t resid_stride, const uint16_t *z, i
                    int64_t gate_stride, float res_scale, const float *w_pre, float eps, int32_t rows, int32_t D,
                    int32_t flags, void *stream) {
   if (rows < 0 || D <= 0 || (flags & ~(int32_t)(KDA_NORM_RESID_BF16 | KDA_NORM_Y_BF16))) return KDA_ERR_INVALID;
-  if (!(eps >= 0.0f) || eps > 3.0e38f || !(res_scale >= -3.0e38f && res_scale <= 3.0e38f)) return KDA_ERR_INVALID;
+  if (!(eps >= 0.0f) || !std::isfinite(eps) || !std::isfinite(res_scale)) return KDA_ERR_INVALID;
   if (D > KDA_NORM_MAX_D) return KDA_ERR_UNSUPPORTED;
   if (rows == 0) return KDA_OK;
   if (!resid || (!z && !y) || (y == nullptr) != (w_pre == nullptr)) return KDA_ERR_INVALID;
