@@ -781,15 +781,15 @@ static bool lin_walks(int32_t B, int32_t n_tok, int32_t H, int32_t dv) {
 // Chunks per segment and the segments past the rows' first ones. Many chunks are
 // shared by about 512 (segment, head) workgroups, two per CU: cutting further
 // moves more states, cutting less leaves CUs idle (us at 256, 512 and 1024
-// workgroups: 8000 tokens x 32 heads of 128 x 128 153, 150, 165; 2 rows of 16384 x 32
-// of 64 x 64 265, 224, 237; 16 ragged rows of 5003 in all 129, 107, 115). Few are cut to about 256, but to
-// no less than 2 and no more than 4 chunks each, where a chunk's latency counts
-// against that of chaining the segments (1024 tokens x 32 heads, 2 and 4 chunks:
-// 37, 43; 2048 x 32: 59, 51; 2048 x 8: 32, 41; 8000 x 8: 67, 56); with rows of
-// under 4 chunks on average not below 4, since rows that need no cut would still
-// pay for three launches (4 rows of 64 tokens x 32 heads: 18, 12.7). Rows of at
-// most that many chunks are one segment. A row of n tokens has at most
-// (n - 1) / 64 chunks after its first, so the rows together have at most
+// workgroups: 8000 tokens x 32 heads of 128 x 128 153, 150, 165; 2 rows of 16384
+// x 32 of 64 x 64 265, 224, 237; 16 ragged rows of 5003 in all 129, 107, 115). Few
+// are cut to about 256, but to no less than 2 and no more than 4 chunks each, where
+// a chunk's latency counts against that of chaining the segments (1024 tokens x 32
+// heads, 2 and 4 chunks: 37, 43; 2048 x 32: 59, 51; 2048 x 8: 32, 41; 8000 x 8: 67,
+// 56); with rows of under 4 chunks on average not below 4, since rows that need no
+// cut would still pay for three launches (4 rows of 64 tokens x 32 heads: 18,
+// 12.7). Rows of at most that many chunks are one segment. A row of n tokens has at
+// most (n - 1) / 64 chunks after its first, so the rows together have at most
 // (n_tok - 1) / 64 / seg segments after their first ones.
 struct LinSplit {
   int32_t seg;

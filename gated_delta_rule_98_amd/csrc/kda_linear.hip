@@ -653,15 +653,16 @@ __global__ __launch_bounds__(lin_threads(DV)) void lin_scan_kernel(LinArgs a) {
 //
 // 8000 tokens x 32 heads of 128 x 128, fp32 out: 88 us once the clock has settled (98
 // to 115 in a process's first calls; with every chunk's inputs resident in L2 a sixth
-// less), so what bounds it is mostly not HBM. A chunk of one head takes a wave 48 MFMAs for S0^T q, 5 for the
-// scores, 18 for their product with v and 48 for the state, and as many cycles of
-// VALU work to split the fp32 operands, in phases that barriers keep apart. Every
-// wave reads all of q, k and the scores from LDS, 0.5 MB a chunk: the LDS is busy
-// 56% of the time (25% in bank conflicts), VALU 40%, MFMA 36%. 8 waves of 16 columns
-// keep 128 registers and so two workgroups per CU. 4 waves of 32 columns, which would
-// halve those reads, spilled hoisted addresses when they were tried (137 us); they
-// have not been timed with the addresses pinned. The transposing reads' two rows
-// apart, which takes a fifth of the conflicts away: the same within 1%.
+// less), so what bounds it is mostly not HBM. A chunk of one head takes a wave 48
+// MFMAs for S0^T q, 5 for the scores, 18 for their product with v and 48 for the
+// state, and as many cycles of VALU work to split the fp32 operands, in phases that
+// barriers keep apart. Every wave reads all of q, k and the scores from LDS, 0.5 MB a
+// chunk: the LDS is busy 56% of the time (25% in bank conflicts), VALU 40%, MFMA 36%.
+// 8 waves of 16 columns keep 128 registers and so two workgroups per CU. 4 waves of
+// 32 columns, which would halve those reads, spilled hoisted addresses when they were
+// tried (137 us); they have not been timed with the addresses pinned. The transposing
+// reads' two rows apart, which takes a fifth of the conflicts away: the same within
+// 1%.
 template <int DK, int DV, bool BF16>
 __global__ __launch_bounds__(lin_threads(DV), 2 * DV / 64) void lin_out_kernel(LinArgs a) {
   constexpr int NT = lin_threads(DV), NW = NT / 64, KB = DK / 32, T = kLinChunk / kLB;

@@ -78,8 +78,8 @@ int kda_lin_decode_step(float *cache, int64_t num_slots, int64_t slot_stride, co
  * ckpt_pos[b] tokens to ckpt[b], 0 = before the prompt, < 0 = none; past the
  * row is KDA_DEVERR_CKPT). Outputs and states agree with successive
  * kda_lin_decode_step calls to fp32 rounding (states, decayed scores and decayed
- * tokens enter products to 2^-133, which rounds those below 2^-109); with KDA_OUT_BF16 each output is
- * the fp32 one rounded to nearest even. tile_w must be 0.
+ * tokens enter products to 2^-133, which cuts bits off those below 2^-109); with
+ * KDA_OUT_BF16 each output is the fp32 one rounded to nearest even. tile_w must be 0.
  * workspace: device memory of at least kda_lin_prefill_workspace() bytes,
  * 16-byte aligned (NULL where that is 0), not shared by calls that may overlap;
  * its contents need no initialization and are dead when the stream has passed
